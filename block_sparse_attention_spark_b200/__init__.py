@@ -14,8 +14,11 @@ import os
 __all__ = ["SparkError", "Params", "lib", "params", "num_selected", "workspace_size",
            "host_workspace_size", "workspace_region", "alloc_workspace", "moments", "reblock",
            "positional_perm", "select", "attn_fwd", "attn_fwd_joint", "forward", "forward_joint",
-           "forward_host", "get_status", "selftest_wait",
-           "LAYOUTS", "SUMMARIES", "TAILS", "WS"]
+           "forward_host", "get_status", "selftest_wait", "RotaryParams", "rotary_params",
+           "rotary_validate", "rotary_workspace_size", "alloc_rotary_workspace", "rotary", "rotary_bwd",
+           "CrossParams", "cross_params", "cross_validate", "cross_workspace_size",
+           "alloc_cross_workspace", "cross_attn", "cross_attn_bwd",
+           "LAYOUTS", "SUMMARIES", "TAILS", "WS", "DTYPES", "PAIRINGS", "SPECTRA"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspark.so")
@@ -25,6 +28,9 @@ SUMMARIES = {"reweight": 0, "meanpool": 1}
 TAILS = {"query": 0, "block": 1}
 WS = {"MQ": 0, "MK": 1, "QMEAN": 2, "PERM": 3, "SEL": 4, "QM": 5, "KM": 6, "KT": 7, "VT": 8,
       "BETA": 9, "UHAT": 10, "PAIRS": 11}
+DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
+PAIRINGS = {"interleaved": 0, "halves": 1}
+SPECTRA = {"axis": 0, "shared": 1}
 STATUS = {0: "SPARK_OK", 1: "SPARK_ERR_INVALID_ARG", 2: "SPARK_ERR_UNSUPPORTED",
           3: "SPARK_ERR_WORKSPACE", 4: "SPARK_ERR_CUDA", 5: "SPARK_ERR_TIMEOUT"}
 
@@ -49,8 +55,42 @@ class Params(ctypes.Structure):
                 f"layout={self.layout}, summary={self.summary}, tail={self.tail})")
 
 
+class RotaryParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("dims", ctypes.c_int32 * 3),
+                ("pairing", ctypes.c_int32), ("spectrum", ctypes.c_int32),
+                ("grid", ctypes.c_int32 * 3), ("theta", ctypes.c_double),
+                ("start", ctypes.c_double * 3), ("scale", ctypes.c_double * 3),
+                ("eps", ctypes.c_double)]
+
+    def __repr__(self):
+        return (f"RotaryParams(B={self.B}, Hq={self.Hq}, Hk={self.Hk}, N={self.N}, d={self.d}, "
+                f"dims={tuple(self.dims)[:self.axes]}, grid={tuple(self.grid)[:self.axes]}, "
+                f"dtype={self.dtype}, pairing={self.pairing}, spectrum={self.spectrum})")
+
+
+class CrossParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_double)]
+
+    def __repr__(self):
+        return (f"CrossParams(B={self.B}, Hq={self.Hq}, Hkv={self.Hkv}, Nq={self.Nq}, Nk={self.Nk}, "
+                f"d={self.d}, dtype={self.dtype}, scale={self.scale})")
+
+
+class View(ctypes.Structure):
+    """A [B,H,N,d] tensor's address and its strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("b", ctypes.c_int64), ("h", ctypes.c_int64),
+                ("n", ctypes.c_int64)]
+
+
 _LIB = None
 _P = ctypes.POINTER(Params)
+_RP = ctypes.POINTER(RotaryParams)
+_CP = ctypes.POINTER(CrossParams)
+_V = ctypes.POINTER(View)
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _i32 = ctypes.c_int32
@@ -76,6 +116,14 @@ _SIGS = {
     "spark_get_status": (_i32, [_vp]),
     "spark_selftest_wait": (_i32, [ctypes.c_int64, _vp]),
     "spark_strerror": (ctypes.c_char_p, [_i32]),
+    "spark_rotary_validate": (_i32, [_RP]),
+    "spark_rotary_workspace_size": (_sz, [_RP]),
+    "spark_rotary": (_i32, [_RP, _V, _V, _vp, _vp, _vp, _V, _V, _vp]),
+    "spark_rotary_bwd": (_i32, [_RP, _V, _V, _V, _V, _vp, _vp, _vp, _V, _V, _vp, _vp, _vp, _sz, _vp]),
+    "spark_cross_validate": (_i32, [_CP]),
+    "spark_cross_workspace_size": (_sz, [_CP, _i32]),
+    "spark_cross_attn": (_i32, [_CP, _V, _V, _V, _vp, _vp, _V, _vp, _vp, _sz, _vp]),
+    "spark_cross_attn_bwd": (_i32, [_CP, _V, _V, _V, _V, _vp, _V, _vp, _vp, _V, _V, _V, _vp, _sz, _vp]),
 }
 
 
@@ -317,6 +365,246 @@ def forward_host(p: Params, q_host, k_host, v_host, out_host, ws, lse_host=None)
                                     _ptr(out_host), _ptr(lse_host), _ptr(ws), ws.numel(),
                                     _stream()), "spark_forward_host")
     return out_host
+
+
+# ------------------------------------------- rotary positions, cross attention
+# Tensors are [B, H, N, d] views: any strides over batch, head and token with
+# the last axis contiguous (a projection's [B, N, H, d] result goes in as
+# x.transpose(1, 2)). All tensors of a call are on one device, the call's
+# kernels on that device's current stream.
+
+def _dtype_of(code):
+    torch = _torch()
+    return (torch.bfloat16, torch.float16, torch.float32)[code]
+
+
+def _on(t, name, device, dtype, shape, contiguous=False):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.device != device or device.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype or tuple(t.shape) != shape or (contiguous and not t.is_contiguous()):
+        kind = "a contiguous" if contiguous else "a"
+        raise TypeError(f"{name} must be {kind} {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _view(t, name, device, dtype, shape):
+    ptr = _on(t, name, device, dtype, shape)
+    b, h, n, one = t.stride()
+    if one != 1:
+        raise TypeError(f"{name}: the last axis must be contiguous")
+    return View(ptr, b, h, n)
+
+
+def _device(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+class _Current:
+    """Makes a device current for a call where it is not."""
+
+    def __init__(self, device):
+        torch = _torch()
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _scratch(ws, size, device, where):
+    torch = _torch()
+    if ws is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    if not isinstance(ws, torch.Tensor) or ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise TypeError(f"{where}: ws must be a contiguous uint8 tensor on {device}")
+    return ws
+
+
+def rotary_params(B, H, N, d, dims, heads_k=None, grid=None, dtype="bf16", pairing="interleaved",
+                  spectrum="axis", theta=10000.0, start=(0.0, 0.0, 0.0), scale=(1.0, 1.0, 1.0),
+                  eps=1e-6) -> RotaryParams:
+    """Parameters of rotary / rotary_bwd for H query and heads_k (default H; 0:
+    none) key heads. dims: rotated values per axis (one to three axes); grid:
+    the tokens' raster grid, as many extents as dims, or None when every call
+    gets positions."""
+    dims = tuple(int(x) for x in dims)
+    axes = len(dims)
+    if not 1 <= axes <= 3:
+        raise ValueError("dims: one to three axes")
+    grid = (0,) * axes if grid is None else tuple(int(x) for x in grid)
+    if len(grid) != axes:
+        raise ValueError("grid: as many extents as dims")
+    i3, d3 = ctypes.c_int32 * 3, ctypes.c_double * 3
+    return RotaryParams(B, H, H if heads_k is None else heads_k, N, d, DTYPES[dtype], axes, i3(*dims),
+                        PAIRINGS[pairing], SPECTRA[spectrum], i3(*grid), float(theta),
+                        d3(*(float(x) for x in start)), d3(*(float(x) for x in scale)), float(eps))
+
+
+def rotary_validate(p: RotaryParams) -> int:
+    return lib().spark_rotary_validate(ctypes.byref(p))
+
+
+def rotary_workspace_size(p: RotaryParams) -> int:
+    """Bytes of workspace rotary_bwd needs when a norm weight is given."""
+    return lib().spark_rotary_workspace_size(ctypes.byref(p))
+
+
+def alloc_rotary_workspace(p: RotaryParams, device="cuda"):
+    n = rotary_workspace_size(p)
+    if n == 0:
+        _check(rotary_validate(p) or 1, "rotary_workspace_size")
+    return _torch().empty(n, dtype=_torch().uint8, device=device)
+
+
+def _rotary_extras(p, device, dtype, positions, q_weight, k_weight):
+    pos = None if positions is None else _on(positions, "positions", device, _torch().float32,
+                                             (p.B, p.N, p.axes), True)
+    wq = None if q_weight is None else _on(q_weight, "q_weight", device, dtype, (p.d,), True)
+    wk = None if k_weight is None else _on(k_weight, "k_weight", device, dtype, (p.d,), True)
+    return pos, wq, wk
+
+
+def rotary(p: RotaryParams, q, k=None, positions=None, q_weight=None, k_weight=None, out=None):
+    """Rotary positions of q [B,Hq,N,d] and k [B,Hk,N,d] (None when heads_k is
+    0), after the per-head RMS norm of those with a weight ([d]). positions:
+    [B,N,axes] float32, default the parameters' grid. Returns (q_out, k_out),
+    contiguous [B,H,N,d] as forward() reads them, or the tensors of
+    out=(q_out, k_out), which may be q and k themselves."""
+    torch = _torch()
+    dev, dt = _device(q, "q"), _dtype_of(p.dtype)
+    qs, ks = (p.B, p.Hq, p.N, p.d), (p.B, p.Hk, p.N, p.d)
+    if (k is None) != (p.Hk == 0):
+        raise TypeError("k: given exactly when the parameters have key heads")
+    vq = _view(q, "q", dev, dt, qs)
+    vk = None if k is None else _view(k, "k", dev, dt, ks)
+    pos, wq, wk = _rotary_extras(p, dev, dt, positions, q_weight, k_weight)
+    if out is None:
+        qo = torch.empty(qs, dtype=dt, device=dev)
+        ko = None if k is None else torch.empty(ks, dtype=dt, device=dev)
+    else:
+        qo, ko = out
+    wqo = _view(qo, "q_out", dev, dt, qs)
+    wko = None if k is None else _view(ko, "k_out", dev, dt, ks)
+    with _Current(dev):
+        _check(lib().spark_rotary(p, vq, vk, pos, wq, wk, wqo, wko, _stream()), "spark_rotary")
+    return qo, ko
+
+
+def rotary_bwd(p: RotaryParams, dq_out, dk_out=None, q=None, k=None, positions=None, q_weight=None,
+               k_weight=None, ws=None):
+    """Gradient of rotary: (dq, dk, dq_weight, dk_weight) from the gradients of
+    its outputs. q and k, its inputs, are needed where that tensor has a
+    weight; dq and dk come in their layout when they are given (contiguous
+    otherwise), weight gradients as float32 [d] (None without a weight)."""
+    torch = _torch()
+    dev, dt = _device(dq_out, "dq_out"), _dtype_of(p.dtype)
+    qs, ks = (p.B, p.Hq, p.N, p.d), (p.B, p.Hk, p.N, p.d)
+    if (dk_out is None) != (p.Hk == 0):
+        raise TypeError("dk_out: given exactly when the parameters have key heads")
+    pos, wq, wk = _rotary_extras(p, dev, dt, positions, q_weight, k_weight)
+    if (wq is not None and q is None) or (wk is not None and p.Hk and k is None):
+        raise TypeError("a tensor with a norm weight is needed for its gradient")
+    vq = None if q is None else _view(q, "q", dev, dt, qs)
+    vk = None if k is None or p.Hk == 0 else _view(k, "k", dev, dt, ks)
+    gq = _view(dq_out, "dq_out", dev, dt, qs)
+    gk = None if dk_out is None else _view(dk_out, "dk_out", dev, dt, ks)
+    dq = torch.empty(qs, dtype=dt, device=dev) if q is None else torch.empty_like(q)
+    dk = None if dk_out is None else torch.empty(ks, dtype=dt, device=dev) if k is None else torch.empty_like(k)
+    dwq = None if wq is None else torch.empty(p.d, dtype=torch.float32, device=dev)
+    dwk = None if wk is None or p.Hk == 0 else torch.empty(p.d, dtype=torch.float32, device=dev)
+    if wq is not None or wk is not None:
+        ws = _scratch(ws, rotary_workspace_size(p), dev, "rotary_bwd")
+    else:
+        ws = None
+    odq = _view(dq, "dq", dev, dt, qs)
+    odk = None if dk is None else _view(dk, "dk", dev, dt, ks)
+    with _Current(dev):
+        _check(lib().spark_rotary_bwd(p, gq, gk, vq, vk, pos, wq, wk, odq, odk, _ptr(dwq), _ptr(dwk), _ptr(ws),
+                                      0 if ws is None else ws.numel(), _stream()), "spark_rotary_bwd")
+    return dq, dk, dwq, dwk
+
+
+def cross_params(B, H, Nq, Nk, d, heads_kv=None, dtype="bf16", scale=None) -> CrossParams:
+    """Parameters of cross_attn / cross_attn_bwd: H query heads over heads_kv
+    (default H) key heads, Nq query tokens over Nk states; scale of the logits
+    (default 1/sqrt(d))."""
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be positive")
+    return CrossParams(B, H, H if heads_kv is None else heads_kv, Nq, Nk, d, DTYPES[dtype],
+                       0.0 if scale is None else float(scale))
+
+
+def cross_validate(p: CrossParams) -> int:
+    return lib().spark_cross_validate(ctypes.byref(p))
+
+
+def cross_workspace_size(p: CrossParams, bwd=False) -> int:
+    return lib().spark_cross_workspace_size(ctypes.byref(p), int(bwd))
+
+
+def alloc_cross_workspace(p: CrossParams, bwd=False, device="cuda"):
+    n = cross_workspace_size(p, bwd)
+    if n == 0:
+        _check(cross_validate(p) or 2, "cross_workspace_size")
+    return _torch().empty(n, dtype=_torch().uint8, device=device)
+
+
+def _cross_masks(p, device, key_len, key_mask):
+    torch = _torch()
+    if key_mask is not None and isinstance(key_mask, torch.Tensor) and key_mask.dtype == torch.bool:
+        key_mask = key_mask.view(torch.uint8)
+    kl = None if key_len is None else _on(key_len, "key_len", device, torch.int32, (p.B,), True)
+    km = None if key_mask is None else _on(key_mask, "key_mask", device, torch.uint8, (p.B, p.Nk), True)
+    return kl, km
+
+
+def cross_attn(p: CrossParams, q, k, v, ws=None, key_len=None, key_mask=None, return_lse=False, out=None):
+    """Attention of q [B,H,Nq,d] over an encoder's k, v [B,heads_kv,Nk,d].
+    key_len: [B] int32, keys kept per item; key_mask: [B,Nk] bool or uint8,
+    true where a key is kept; both: their intersection. Rows without a key give
+    zeros (lse -inf). Returns out (contiguous, or the tensor out=, of any
+    layout), with return_lse also lse [B,H,Nq] float32."""
+    torch = _torch()
+    dev, dt = _device(q, "q"), _dtype_of(p.dtype)
+    qs, ks = (p.B, p.Hq, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+    vq, vk, vv = _view(q, "q", dev, dt, qs), _view(k, "k", dev, dt, ks), _view(v, "v", dev, dt, ks)
+    kl, km = _cross_masks(p, dev, key_len, key_mask)
+    if out is None:
+        out = torch.empty(qs, dtype=dt, device=dev)
+    vo = _view(out, "out", dev, dt, qs)
+    lse = torch.empty(qs[:3], dtype=torch.float32, device=dev) if return_lse else None
+    ws = _scratch(ws, cross_workspace_size(p), dev, "cross_attn")
+    with _Current(dev):
+        _check(lib().spark_cross_attn(p, vq, vk, vv, kl, km, vo, _ptr(lse), ws.data_ptr(), ws.numel(), _stream()),
+               "spark_cross_attn")
+    return (out, lse) if return_lse else out
+
+
+def cross_attn_bwd(p: CrossParams, q, k, v, out, lse, dout, ws=None, key_len=None, key_mask=None):
+    """Gradient of cross_attn: (dq, dk, dv), in the layouts of q, k and v, from
+    dout and the out and lse that cross_attn gave for the same arguments."""
+    torch = _torch()
+    dev, dt = _device(q, "q"), _dtype_of(p.dtype)
+    qs, ks = (p.B, p.Hq, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+    views = [_view(t, n, dev, dt, s) for t, n, s in ((q, "q", qs), (k, "k", ks), (v, "v", ks), (out, "out", qs),
+                                                     (dout, "dout", qs))]
+    pl = _on(lse, "lse", dev, torch.float32, qs[:3], True)
+    kl, km = _cross_masks(p, dev, key_len, key_mask)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    grads = [_view(t, n, dev, dt, s) for t, n, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks))]
+    ws = _scratch(ws, cross_workspace_size(p, True), dev, "cross_attn_bwd")
+    with _Current(dev):
+        _check(lib().spark_cross_attn_bwd(p, *views[:4], pl, views[4], kl, km, *grads, ws.data_ptr(), ws.numel(),
+                                          _stream()), "spark_cross_attn_bwd")
+    return dq, dk, dv
 
 
 def selftest_wait(limit_ns: int):

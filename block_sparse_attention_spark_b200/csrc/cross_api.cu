@@ -1,0 +1,74 @@
+// Cross attention entry points: checks, choice of the kernel, workspace.
+#include <math.h>
+
+#include "cross.h"
+
+namespace spark {
+namespace cross {
+
+static spark_status validate(const spark_cross_params* p) {
+  if (p == nullptr || p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->Nq < 1 || p->Nk < 1 || p->d < 1)
+    return SPARK_ERR_INVALID_ARG;
+  if (p->Hq % p->Hkv != 0 || !isfinite(p->scale) || p->scale < 0.0) return SPARK_ERR_INVALID_ARG;
+  if (p->dtype < SPARK_BF16 || p->dtype > SPARK_FP32) return SPARK_ERR_INVALID_ARG;
+  if (p->dtype == SPARK_FP32) return SPARK_ERR_UNSUPPORTED;
+  if (p->d != 64 && p->d != 128) return SPARK_ERR_UNSUPPORTED;
+  if (p->Nq > SPARK_CROSS_MAX_TOKENS || p->Nk > SPARK_CROSS_MAX_TOKENS) return SPARK_ERR_UNSUPPORTED;
+  if ((int64_t)p->B * p->Hq > 65535 || (int64_t)p->B * p->Hq * p->Nq > INT32_MAX ||
+      (int64_t)p->B * p->Hkv * p->Nk > INT32_MAX)
+    return SPARK_ERR_UNSUPPORTED;
+  return SPARK_OK;
+}
+
+static Problem problem(const spark_cross_params* p) {
+  Problem c = {};
+  c.B = p->B; c.Hq = p->Hq; c.Hkv = p->Hkv; c.G = p->Hq / p->Hkv;
+  c.Nq = p->Nq; c.Nk = p->Nk; c.d = p->d;
+  c.fp16 = p->dtype == SPARK_FP16;
+  c.scale = (float)(p->scale > 0.0 ? p->scale : 1.0 / sqrt((double)p->d));
+  return c;
+}
+
+}  // namespace cross
+}  // namespace spark
+
+using namespace spark;
+
+extern "C" {
+
+spark_status spark_cross_validate(const spark_cross_params* p) { return cross::validate(p); }
+
+size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd) {
+  if (cross::validate(p) != SPARK_OK || (bwd && p->dtype != SPARK_BF16)) return 0;
+  const cross::Problem c = cross::problem(p);
+  return cross::few_workspace(c) + 256;
+}
+
+spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, const spark_view* k,
+                              const spark_view* v, const int32_t* key_len, const uint8_t* key_mask,
+                              const spark_view* out, float* lse, void* ws, size_t ws_bytes,
+                              cudaStream_t stream) {
+  const spark_status vs = cross::validate(p);
+  if (vs != SPARK_OK) return vs;
+  cross::Problem c = cross::problem(p);
+  if (!make_view(q, c.B, c.Hq, c.Nq, c.d, 2, false, &c.q) || !make_view(k, c.B, c.Hkv, c.Nk, c.d, 2, false, &c.k) ||
+      !make_view(v, c.B, c.Hkv, c.Nk, c.d, 2, false, &c.v) || !make_view(out, c.B, c.Hq, c.Nq, c.d, 2, true, &c.out))
+    return SPARK_ERR_INVALID_ARG;
+  if (((uintptr_t)key_len & 3u) != 0 || ((uintptr_t)lse & 3u) != 0) return SPARK_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws)) return SPARK_ERR_INVALID_ARG;
+  if (ws_bytes < spark_cross_workspace_size(p, 0)) return SPARK_ERR_WORKSPACE;
+  c.key_len = key_len;
+  c.key_mask = key_mask;
+  c.lse = lse;
+  c.status = device_status();
+  return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+}
+
+}  // extern "C"
+
+extern "C" spark_status spark_cross_attn_bwd(const spark_cross_params*, const spark_view*, const spark_view*,
+                                             const spark_view*, const spark_view*, const float*, const spark_view*,
+                                             const int32_t*, const uint8_t*, const spark_view*, const spark_view*,
+                                             const spark_view*, void*, size_t, cudaStream_t) {
+  return SPARK_ERR_UNSUPPORTED;
+}

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "plan.h"
+#include "views.h"
 
 namespace spark {
 
@@ -20,6 +21,8 @@ static int* status_ptr() {
   if (cudaGetSymbolAddress(&p, g_spark_status) != cudaSuccess) return nullptr;
   return static_cast<int*>(p);
 }
+
+int* device_status() { return status_ptr(); }
 
 static int num_selected_impl(int nb, double ratio, int blocks) {
   if (blocks > 0) return std::min(blocks, nb);

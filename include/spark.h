@@ -308,6 +308,124 @@ enum {
 };
 size_t spark_workspace_region(const spark_params* p, int32_t region, size_t* bytes);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the self-attention of a video transformer layer: the rotary
+ * positions (and per-head RMS norm) its q and k get, and its second attention,
+ * over an encoder's states of another length; each with its gradient.
+ *
+ * Tensors here are views: [B,H,N,d] elements with the last axis contiguous and
+ * the strides of the other three given in elements, so a projection's result
+ * [B,N,H,d] is read where it lies and an output can be written in the next
+ * projection's layout. Rules, checked on the host (SPARK_ERR_INVALID_ARG):
+ * base address 16-byte aligned, every stride a multiple of 16 bytes and >= 0
+ * (the token stride at least d when there is more than one token; batch and
+ * head strides of a read tensor may be 0, a shared row); a written view
+ * must not overlap itself. Strides of axes of extent 1 are not looked at. All
+ * pointers are on the current device. d is 64 or 128. Everything else is as
+ * for the calls above: asynchronous on the stream, no allocation, no fallback.
+ * Sizes below 1 are SPARK_ERR_INVALID_ARG (masks may still leave no key). */
+typedef struct {
+  const void* data;
+  int64_t b, h, n;             /* strides in elements */
+} spark_view;
+
+enum { SPARK_BF16 = 0, SPARK_FP16 = 1, SPARK_FP32 = 2 };
+
+/* Which two values of a row one angle turns. */
+enum {
+  SPARK_ROTARY_INTERLEAVED = 0,  /* (2i, 2i + 1) */
+  SPARK_ROTARY_HALVES = 1        /* (i, i + R/2), R = all rotated values */
+};
+/* Frequency of pair i, the j-th of its axis with dims[a] rotated values. */
+enum {
+  SPARK_ROTARY_PER_AXIS = 0,   /* theta^(-2j / dims[a]): every axis has the whole spectrum */
+  SPARK_ROTARY_SHARED = 1      /* theta^(-2i / R): the axes share one spectrum */
+};
+
+typedef struct {
+  int32_t B, Hq, Hk, N, d;     /* Hk = 0: q alone */
+  int32_t dtype;               /* SPARK_BF16 | SPARK_FP16 | SPARK_FP32: all tensors and norm weights */
+  int32_t axes;                /* 1..3 */
+  int32_t dims[3];             /* rotated values of a row per axis, even, >= 0, R = sum <= d; pairs
+                                  belong to the axes in turn, values past R are kept */
+  int32_t pairing, spectrum;   /* SPARK_ROTARY_* */
+  int32_t grid[3];             /* no positions given: N = product of grid[0..axes), raster order
+                                  (last axis fastest, as for spark_positional_perm) */
+  double theta;                /* > 0 */
+  double start[3], scale[3];   /* angle = (start[a] + scale[a] * position) * frequency */
+  double eps;                  /* of the RMS norm, >= 0 */
+} spark_rotary_params;
+
+/* Rotary positions of q and k, with the per-head RMS norm before them.
+ * Row x of head h at token n: with a weight w (q_weight for q, k_weight for k;
+ * NULL: no norm) x_i becomes x_i w_i / sqrt(mean x^2 + eps), then each pair
+ * (u, v) becomes (u cos - v sin, u sin + v cos). Angles are formed in 64 bits,
+ * the rest in 32, rounded once. In place (the output view equal to the input
+ * view) is allowed; other overlaps are not.
+ *   q, k       : views [B,Hq,N,d], [B,Hk,N,d] (k, k_out NULL when Hk = 0)
+ *   positions  : [B,N,axes] float32 contiguous device, or NULL (grid)
+ *   weights    : [d] of the tensors' type, 16-byte aligned, or NULL
+ * One kernel launch. */
+spark_status spark_rotary(const spark_rotary_params* p, const spark_view* q, const spark_view* k,
+                          const float* positions, const void* q_weight, const void* k_weight,
+                          const spark_view* q_out, const spark_view* k_out, cudaStream_t stream);
+
+/* Its gradient: dq, dk from the gradients of both outputs, and the weights'
+ * gradients [d] float32 (summed over all rows in a fixed order: equal calls
+ * give equal bits). q and k (the inputs of spark_rotary) are read only where
+ * that tensor has a weight, else may be NULL; dq may be the view dq_out itself.
+ *   ws : workspace of spark_rotary_workspace_size() bytes, needed with a
+ *        weight (scratch; calls that may overlap need one each) */
+size_t spark_rotary_workspace_size(const spark_rotary_params* p);
+spark_status spark_rotary_bwd(const spark_rotary_params* p, const spark_view* dq_out,
+                              const spark_view* dk_out, const spark_view* q, const spark_view* k,
+                              const float* positions, const void* q_weight, const void* k_weight,
+                              const spark_view* dq, const spark_view* dk, float* dq_weight,
+                              float* dk_weight, void* ws, size_t ws_bytes, cudaStream_t stream);
+spark_status spark_rotary_validate(const spark_rotary_params* p);
+
+#define SPARK_CROSS_MAX_TOKENS (1 << 22)
+
+typedef struct {
+  int32_t B, Hq, Hkv;          /* Hq a multiple of Hkv: query head h reads key head h / (Hq / Hkv) */
+  int32_t Nq, Nk, d;           /* any lengths from 1 to SPARK_CROSS_MAX_TOKENS */
+  int32_t dtype;               /* SPARK_BF16 | SPARK_FP16 (the gradient: SPARK_BF16) */
+  double scale;                /* of the logits; 0: 1/sqrt(d) */
+} spark_cross_params;
+
+/* Dense attention of Nq tokens over the Nk states of an encoder:
+ * out = softmax(scale q k^T over the kept keys) v, lse its natural-log
+ * denominators. Key j of item b is kept if j < key_len[b] and key_mask[b,j]
+ * != 0 (a NULL one keeps all). What stands in the rows of k and v that are not
+ * kept is never used, infinities and NaN included. A row without a kept key
+ * gives zeros and lse = -inf. A key_len below 0 or above Nk counts as 0 or Nk
+ * and is reported by spark_get_status() as SPARK_ERR_UNSUPPORTED.
+ *   q, k, v, out : views [B,Hq,Nq,d], [B,Hkv,Nk,d] (k and v), [B,Hq,Nq,d]
+ *   key_len      : [B] int32 device or NULL
+ *   key_mask     : [B,Nk] bytes device, contiguous, or NULL
+ *   lse          : [B,Hq,Nq] float32 device or NULL
+ *   ws           : workspace of spark_cross_workspace_size(p, 0) bytes (scratch;
+ *                  calls that may overlap need one each)
+ * P is rounded to the tensors' type for P V, sums and statistics are float32. */
+size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd);
+spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, const spark_view* k,
+                              const spark_view* v, const int32_t* key_len, const uint8_t* key_mask,
+                              const spark_view* out, float* lse, void* ws, size_t ws_bytes,
+                              cudaStream_t stream);
+
+/* Its gradient: dq, dk, dv from the gradient dout of out, with out and lse as
+ * spark_cross_attn gave them. Rows of dk and dv that are not kept are zero; a
+ * shared key head gets the sum over its query heads. Equal calls give equal
+ * bits (no atomics). bf16 only: the products P (dO V^T - D) of small
+ * gradients fall below fp16's normal range (SPARK_ERR_UNSUPPORTED).
+ *   ws : workspace of spark_cross_workspace_size(p, 1) bytes */
+spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view* q, const spark_view* k,
+                                  const spark_view* v, const spark_view* out, const float* lse,
+                                  const spark_view* dout, const int32_t* key_len, const uint8_t* key_mask,
+                                  const spark_view* dq, const spark_view* dk, const spark_view* dv,
+                                  void* ws, size_t ws_bytes, cudaStream_t stream);
+spark_status spark_cross_validate(const spark_cross_params* p);
+
 /* Diagnostic (the pages have no counterpart): checks that a device-side
  * timeout surfaces as an error and leaves the context usable. One warp
  * allocates tensor memory, waits through the bounded-wait routine every
