@@ -23,5 +23,32 @@ struct Problem {
 size_t few_workspace(const Problem& p);
 cudaError_t launch_few(const Problem& p, void* ws, cudaStream_t s);
 
+// Many query rows: 128 rows per tile (tcgen05). Kept keys are the first
+// key_len[b] of an item; key_mask is not looked at.
+size_t many_workspace(const Problem& p);
+cudaError_t launch_many(const Problem& p, void* ws, cudaStream_t s);
+
+// The kept keys of each item moved to the front: k and v become contiguous
+// [B,Hkv,Nk,d] copies in ws whose first count[b] rows are the kept ones in
+// order; place[b,j] is the row key j went to, or -1.
+struct Packed {
+  size_t bytes, off_k, off_v, off_count, off_place;
+};
+Packed pack_plan(const Problem& p);
+cudaError_t launch_pack(const Problem& p, const Packed& pk, void* ws, cudaStream_t s);
+
+inline size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+#ifdef __CUDACC__
+// Length of item b, clamped; `report` says a bad one to the status word.
+__device__ __forceinline__ int item_len(const int32_t* key_len, int Nk, int b, int* status, bool report) {
+  if (key_len == nullptr) return Nk;
+  const int n = key_len[b];
+  if (n >= 0 && n <= Nk) return n;
+  if (report && status) atomicOr(status, 4);
+  return n < 0 ? 0 : Nk;
+}
+#endif
+
 }  // namespace cross
 }  // namespace spark

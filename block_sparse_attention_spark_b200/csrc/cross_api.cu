@@ -29,6 +29,16 @@ static Problem problem(const spark_cross_params* p) {
   return c;
 }
 
+// At most 32 rows per key head (query heads of the group times tokens): tiles
+// of 16 rows that read K and V once each; more: tiles of 128 rows of a head.
+static bool few_rows(const Problem& c) { return (int64_t)c.G * c.Nq <= 32; }
+
+// With a key mask the tensor-core kernels get the kept keys packed to the
+// front (the masks of a call are not known here: the size covers both).
+static size_t forward_workspace(const Problem& c) {
+  return few_rows(c) ? few_workspace(c) : align_up(many_workspace(c)) + pack_plan(c).bytes;
+}
+
 }  // namespace cross
 }  // namespace spark
 
@@ -41,7 +51,7 @@ spark_status spark_cross_validate(const spark_cross_params* p) { return cross::v
 size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd) {
   if (cross::validate(p) != SPARK_OK || (bwd && p->dtype != SPARK_BF16)) return 0;
   const cross::Problem c = cross::problem(p);
-  return cross::few_workspace(c) + 256;
+  return cross::forward_workspace(c) + 256;
 }
 
 spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, const spark_view* k,
@@ -61,7 +71,17 @@ spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, 
   c.key_mask = key_mask;
   c.lse = lse;
   c.status = device_status();
-  return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  if (cross::few_rows(c)) return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  if (c.key_mask != nullptr) {
+    char* at = static_cast<char*>(ws) + cross::align_up(cross::many_workspace(c));
+    const cross::Packed pk = cross::pack_plan(c);
+    if (cross::launch_pack(c, pk, at, stream) != cudaSuccess) return SPARK_ERR_CUDA;
+    const int64_t head = (int64_t)c.Nk * c.d;
+    c.k = View{at + pk.off_k, c.Hkv * head, head, c.d};
+    c.v = View{at + pk.off_v, c.Hkv * head, head, c.d};
+    c.key_len = reinterpret_cast<const int32_t*>(at + pk.off_count);
+  }
+  return cross::launch_many(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -82,15 +82,6 @@ __device__ __forceinline__ void put(char* dst, float v) {
   else *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(v);
 }
 
-// Length of item b, clamped; the first block of the item reports a bad one.
-__device__ __forceinline__ int item_len(const Problem& p, int b, bool report) {
-  if (p.key_len == nullptr) return p.Nk;
-  const int n = p.key_len[b];
-  if (n >= 0 && n <= p.Nk) return n;
-  if (report) set_status(p.status, STATUS_BAD_INPUT);
-  return n < 0 ? 0 : p.Nk;
-}
-
 template <int D, bool H>
 __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a) {
   using L = Lay<D>;
@@ -101,7 +92,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
   const int tile = blockIdx.x, split = blockIdx.y, bk = blockIdx.z;
   const int b = bk / p.Hkv, hk = bk % p.Hkv;
   const uint32_t sq = smem_u32(smem), ring = sq + L::Q + warp * L::WARP;
-  const int len = item_len(p, b, tid == 0 && tile == 0 && split == 0 && hk == 0);
+  const int len = item_len(p.key_len, p.Nk, b, p.status, tid == 0 && tile == 0 && split == 0 && hk == 0);
   const int k_end = min(len, (split + 1) * a.per_split);
 
   // Q rows, zeros past the last

@@ -1,0 +1,563 @@
+// Cross attention of many query rows on the sm_100a tensor cores.
+//
+// One persistent CTA per SM. A work item is two tiles of 128 query rows of one
+// key head (each tile's rows are tokens of one query head) against all the
+// kept keys of that head, or against one share of them when there are fewer
+// tiles than SMs (the shares are joined by join_kernel). K and V stream in
+// tiles of 128 keys through one ring of five 32 KB stages that both row tiles
+// read, which halves the L2 traffic of one tile alone (at 72,576 queries by
+// 512 keys one row tile per CTA would ask 13 TB/s of it).
+//
+// TMEM (512 columns): S of the two tiles at 0 and 128, O at 256 and 384; P
+// (16 bits, two keys a column) overwrites the first half of its S. One thread
+// issues, in turn for the two tiles, P_j V_j and then S_{j+1} = Q K_{j+1}^T:
+// while the tensor cores work for one tile, the other tile's four warps (one
+// thread per row) turn S into P. MMAs of one thread complete in issue order,
+// so S_{j+1} arriving says that P_j V_j is done: O may be rescaled, the next
+// tile's first S may overwrite P, without further barriers. The next item's Q
+// and K are loaded while this one's last tiles run, and its first S is issued before
+// the row tile's O has been written out.
+//
+// The softmax is online with a lazy reference: the row's reference maximum
+// moves (and O is rescaled in TMEM) only when a logit passes it by 2^8. Sums
+// and maxima are float32; P is rounded to the tensors' type, the operand type
+// of the MMA. The last tile of an item runs with N (and for P V, K) cut to the
+// next multiple of 16 of its keys; V rows between are zeroed in shared memory,
+// whatever they hold, because 0 * NaN is NaN.
+//
+// Every wait is bounded (2 s): on expiry the status word is set, copies and
+// MMAs in flight are waited for (bounded again), TMEM is freed, the kernel returns.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "cross.h"
+#include "tc_ptx.cuh"
+#include "tma_map.h"
+
+namespace spark {
+namespace cross {
+namespace many {
+
+using namespace tc;
+
+constexpr int ROWS = 128, KEYS = 128, SLOTS = 2;
+constexpr int SM_WARPS = 4 * SLOTS, TMA_WARP = SM_WARPS, MMA_WARP = SM_WARPS + 1;
+constexpr int THREADS = 32 * (SM_WARPS + 4);      // two warps of the last group stay idle
+// A thread is launched with 168 registers (three warps per scheduler); the
+// softmax needs about 200, the other group little: 256 * 208 + 128 * 88 = 384 * 168.
+constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 208, OTHER_REGS = 88;
+static_assert(SM_WARPS * 32 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * LAUNCH_REGS, "registers the block owns");
+constexpr float LAZY = 8.0f;                 // log2 units
+constexpr uint32_t O_COL = 256;
+
+struct Args {
+  TensorMap q, k, v;
+  View out;
+  const int32_t* key_len;
+  float* lse;
+  int* status;
+  int B, Hq, Hkv, G, Nq, Nk;
+  int tokens;                                // row tiles per head
+  int pairs;                                 // work items per key head: ceil(G * tokens / 2)
+  int splits;
+  int items;                                 // B * Hkv * pairs * splits
+  float sl2;                                 // scale * log2 e
+  int wide;                                  // out rows take 32-byte stores
+  float* part;                               // splits > 1: [items][2][128][d] unnormalised O
+  float2* stat;                              // [items][2][128] (reference, sum)
+};
+
+template <int D>
+struct Lay {
+  static constexpr int ATOMS = D / 64;
+  static constexpr int ATOM = 128 * 128;               // 128 rows x 64 values
+  static constexpr int TILE = ATOM * ATOMS;            // Q tile = K tile = V tile
+  static constexpr int STAGES = 5;
+  static constexpr int SMEM = (SLOTS + STAGES) * TILE + 1024;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int n, int h, int b,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(n), "r"(h), "r"(b), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <bool H>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (H) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// A work item: its key head, its share of the keys and the two row tiles.
+struct Item {
+  int b, hk, pair, k0, valid, tiles;         // first key tile, kept keys of the item, key tiles of the share
+};
+__device__ __forceinline__ Item item_of(const Args& a, int it) {
+  Item w;
+  const int split = it % a.splits, u = it / a.splits;
+  w.pair = u % a.pairs;
+  const int bk = u / a.pairs;
+  w.b = bk / a.Hkv;
+  w.hk = bk % a.Hkv;
+  w.valid = item_len(a.key_len, a.Nk, w.b, nullptr, false);
+  const int all = (w.valid + KEYS - 1) / KEYS, per = (all + a.splits - 1) / a.splits;
+  w.k0 = split * per;
+  w.tiles = max(0, min(per, all - w.k0));
+  return w;
+}
+
+template <int D, bool H>
+__global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Args a) {
+  using L = Lay<D>;
+  constexpr int NBAR = 10 + 2 * L::STAGES + 1;
+  constexpr uint32_t FMT = H ? 0u : 1u;
+  constexpr uint32_t IDESC = (1u << 4) | (FMT << 7) | (FMT << 10) | ((uint32_t)(ROWS >> 4) << 24);
+  constexpr uint32_t IDESC_O = IDESC | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[NBAR];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bar0 = smem_u32(&bars[0]);
+  auto q_full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto q_empty = [&](int s) { return bar0 + 8u * (uint32_t)(2 + s); };
+  auto s_full = [&](int s) { return bar0 + 8u * (uint32_t)(4 + s); };
+  auto p_full = [&](int s) { return bar0 + 8u * (uint32_t)(6 + s); };
+  // O has a barrier of its own: the next item's first S may arrive before the
+  // warps have looked at this one's O, and a parity wait must not fall two phases behind
+  auto o_full = [&](int s) { return bar0 + 8u * (uint32_t)(8 + s); };
+  auto full = [&](int i) { return bar0 + 8u * (uint32_t)(10 + i); };
+  auto empty = [&](int i) { return bar0 + 8u * (uint32_t)(10 + L::STAGES + i); };
+  const uint32_t drain = bar0 + 8u * (uint32_t)(10 + 2 * L::STAGES);
+  auto sQ = [&](int s) { return base + (uint32_t)(s * L::TILE); };
+  auto sKV = [&](int i) { return base + (uint32_t)((SLOTS + i) * L::TILE); };
+
+  if (tid == 0) {
+    abort_sh = 0;
+    for (int i = 0; i < NBAR; ++i) mbar_init(bar0 + 8u * i, (i == 6 || i == 7) ? 4 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_sh)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_sh;
+  const int row_tiles = a.G * a.tokens;
+
+  if (warp < SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+  if (warp < SM_WARPS) {
+    // ------------------------------------------------ softmax and output, one thread per row
+    const int s = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t sc = tb + 128u * (uint32_t)s, oc = tb + O_COL + 128u * (uint32_t)s;
+    const uint64_t sc2 = f2(a.sl2, a.sl2);
+    uint32_t ns = 0, no = 0;                 // S tiles and O's seen
+    bool ok = true;
+    if (a.key_len != nullptr && blockIdx.x == 0 && s == 0)
+      for (int b = r; b < a.B; b += ROWS) item_len(a.key_len, a.Nk, b, a.status, true);
+    for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+      const Item w = item_of(a, it);
+      const int t = 2 * w.pair + s;
+      if (t >= row_tiles) continue;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; ok && j < w.tiles; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full(s), ns & 1u, a.status));
+        ++ns;
+        if (!ok) break;
+        fence_after();
+        uint32_t sv[KEYS];
+#pragma unroll
+        for (int c = 0; c < KEYS / 32; ++c) tmem_ld32p(sc + 32u * c, sv + 32 * c);
+        tmem_ld_wait();
+        const int valid = w.valid - (w.k0 + j) * KEYS;
+        if (valid < KEYS) {
+#pragma unroll
+          for (int c = 0; c < KEYS; ++c)
+            if (c >= valid) sv[c] = 0xff800000u;           // -inf
+        }
+        float mc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mc[i] = fmaxf(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+#pragma unroll
+        for (int c = 16; c < KEYS; c += 16)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mc[i] = max3(mc[i], __uint_as_float(sv[c + 2 * i]), __uint_as_float(sv[c + 2 * i + 1]));
+        const float mt = fmaxf(fmaxf(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5])), fmaxf(mc[6], mc[7])) * a.sl2;
+        float m_new = m, corr = 1.f;
+        bool resc = false;
+        if (m == -INFINITY) {
+          m_new = mt;
+        } else if (mt > m + LAZY) {
+          m_new = mt;
+          corr = ex2(m - mt);
+          resc = true;
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+          // P_{j-1} V_{j-1} is done (S_j came after it), P_j V_j not issued yet
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32p(oc + 32u * cc, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            tmem_st32p(oc + 32u * cc, o);
+          }
+        }
+        // a row whose logits are all -inf so far: exp2(-inf - 0) = 0 (no branch here:
+        // the stores below are collective, and rows of a warp may differ in this)
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const uint64_t nm2 = f2(-ref, -ref);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            float u0, u1;
+            unf2(ffma2(f2(__uint_as_float(sv[64 * hf + c]), __uint_as_float(sv[64 * hf + c + 1])), sc2, nm2), u0, u1);
+            const float p0 = ex2(u0), p1 = ex2(u1);
+            acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], f2(p0, p1));
+            pw[c >> 1] = pack2<H>(p0, p1);
+          }
+          tmem_st32p(sc + 32u * hf, pw);
+        }
+        float r0, r1, r2, r3;
+        unf2(fadd2(acc[0], acc[1]), r0, r1);
+        unf2(fadd2(acc[2], acc[3]), r2, r3);
+        const float rs = (r0 + r2) + (r1 + r3);
+        l = l * corr + rs;
+        m = m_new;
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(s));
+      }
+      if (!ok) break;
+      // ---- O of this row tile
+      if (w.tiles > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_full(s), no & 1u, a.status));
+        ++no;
+        if (!ok) break;
+        fence_after();
+      }
+      const int g = t / a.tokens, n = (t % a.tokens) * ROWS + r;
+      const bool live = n < a.Nq;
+      const int h = w.hk * a.G + g;
+      if (a.splits > 1) {
+        float* dst = a.part + ((size_t)it * SLOTS + s) * ROWS * D + (size_t)r * D;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          if (w.tiles > 0) {
+            tmem_ld32p(oc + 32u * cc, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store32(dst + 32 * cc + e, o + e);
+          }
+        }
+        if (live) a.stat[((size_t)it * SLOTS + s) * ROWS + r] = make_float2(m, l);
+      } else {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        char* dst = a.out.data + 2 * (w.b * a.out.b + h * a.out.h + (int64_t)n * a.out.n);
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32], pk[16];
+          if (w.tiles > 0) {
+            tmem_ld32p(oc + 32u * cc, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[e] = pack2<H>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (live) {
+            if (a.wide) {
+              store32(dst + 64 * cc, pk);
+              store32(dst + 64 * cc + 32, pk + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(dst + 64 * cc + 16 * e) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            }
+          }
+        }
+        if (live && a.lse != nullptr)
+          a.lse[((size_t)w.b * a.Hq + h) * a.Nq + n] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
+      fence_before();                        // O has been read: ordered before the next P's arrival
+    }
+    if (!ok) atomicExch(&abort_sh, 1);
+  } else if (warp == TMA_WARP) {
+    // ------------------------------------------------ loads: Q of both tiles, K_0, V_0, K_1, V_1, ...
+    if (lane == 0) {
+      uint32_t nk = 0, nq[SLOTS] = {0, 0};   // tiles issued
+      bool ok = true;
+      for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+        const Item w = item_of(a, it);
+        if (w.tiles == 0) continue;
+        for (int s = 0; ok && s < SLOTS; ++s) {
+          const int t = 2 * w.pair + s;
+          if (t >= row_tiles) continue;
+          if (nq[s] > 0) ok = mbar_wait(q_empty(s), (nq[s] - 1) & 1u, a.status);
+          if (!ok || *(volatile int*)&abort_sh) { ok = false; break; }
+          const int h = w.hk * a.G + t / a.tokens, n = (t % a.tokens) * ROWS;
+          mbar_arrive_tx(q_full(s), L::TILE);
+#pragma unroll
+          for (int x = 0; x < L::ATOMS; ++x)
+            tma_load_4d(sQ(s) + x * L::ATOM, &a.q.map, 64 * x, n, a.q.h_on ? h : 0, a.q.b_on ? w.b : 0, q_full(s));
+          ++nq[s];
+        }
+        for (int j = 0; ok && j < 2 * w.tiles; ++j) {
+          const int i = nk % L::STAGES;
+          if (nk >= L::STAGES) ok = mbar_wait(empty(i), (nk / L::STAGES - 1) & 1u, a.status);
+          if (!ok || *(volatile int*)&abort_sh) { ok = false; break; }
+          const TensorMap& m = (j & 1) ? a.v : a.k;
+          mbar_arrive_tx(full(i), L::TILE);
+#pragma unroll
+          for (int x = 0; x < L::ATOMS; ++x)
+            tma_load_4d(sKV(i) + x * L::ATOM, &m.map, 64 * x, (w.k0 + (j >> 1)) * KEYS, m.h_on ? w.hk : 0,
+                        m.b_on ? w.b : 0, full(i));
+          ++nk;
+        }
+      }
+      // every copy has landed before this CTA's shared memory goes
+      for (int s = 0; s < SLOTS; ++s)
+        if (nq[s] > 0) mbar_wait(q_full(s), (nq[s] - 1) & 1u, a.status);
+      for (uint32_t x = nk > L::STAGES ? nk - L::STAGES : 0; x < nk; ++x)
+        mbar_wait(full(x % L::STAGES), (x / L::STAGES) & 1u, a.status);
+      if (!ok) atomicExch(&abort_sh, 1);
+    }
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------ MMAs (all lanes wait, lane 0 issues)
+    uint32_t nk = 0, nq[SLOTS] = {0, 0}, np[SLOTS] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status));
+      fence_after();
+      return ok;
+    };
+    // S of a slot from K in stage i, n keys (a multiple of 16)
+    auto issue_s = [&](int s, int i, int n) {
+      if (lane != 0) return;
+      const uint64_t dq = sdesc(sQ(s), 16, 1024), dk = sdesc(sKV(i), 16, 1024);
+      const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint64_t o = (uint64_t)(((ks >> 2) * L::ATOM + (ks & 3) * 32) >> 4);
+        mma_f16(tmem + 128u * (uint32_t)s, dq + o, dk + o, idesc, ks > 0 ? 1u : 0u);
+      }
+    };
+    for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+      const Item w = item_of(a, it);
+      if (w.tiles == 0) continue;
+      const int slots = 2 * w.pair + 1 < row_tiles ? 2 : 1;
+      const int last = w.valid - (w.k0 + w.tiles - 1) * KEYS;       // keys of the last tile
+      auto n16 = [&](int j) { return j == w.tiles - 1 && last < KEYS ? (last + 15) & ~15 : KEYS; };
+      if (!wait(full(nk % L::STAGES), (nk / L::STAGES) & 1u)) break;
+      for (int s = 0; ok && s < slots; ++s) {
+        if (!wait(q_full(s), nq[s] & 1u)) break;
+        ++nq[s];
+        issue_s(s, nk % L::STAGES, n16(0));
+        if (lane == 0) {
+          mma_commit(s_full(s));
+          if (w.tiles == 1) mma_commit(q_empty(s));
+          if (s == slots - 1) mma_commit(empty(nk % L::STAGES));
+        }
+      }
+      ++nk;
+      for (int j = 0; ok && j < w.tiles; ++j) {
+        // V_j in stage nk, K_{j+1} in the next one
+        const int iv = nk % L::STAGES, ik = (nk + 1) % L::STAGES;
+        const bool more = j + 1 < w.tiles;
+        if (!wait(full(iv), (nk / L::STAGES) & 1u)) break;
+        const int n = n16(j);
+        if (!more && (last & 15) != 0) {
+          // rows of V past the last kept key, up to the MMA's K
+          for (int e = lane; e < (n - last) * (D / 8); e += 32) {
+            const int row = last + e / (D / 8), c = e % (D / 8);
+            const uint32_t at = sKV(iv) + (c >> 3) * L::ATOM + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        if (more && !wait(full(ik), ((nk + 1) / L::STAGES) & 1u)) break;
+        for (int s = 0; ok && s < slots; ++s) {
+          if (!wait(p_full(s), np[s] & 1u)) break;
+          ++np[s];
+          if (lane == 0) {
+            const uint64_t dv = sdesc(sKV(iv), L::ATOM, 1024);
+            const uint32_t pa = tmem + 128u * (uint32_t)s, od = tmem + O_COL + 128u * (uint32_t)s;
+            for (int kk = 0; kk < n / 16; ++kk)
+              mma_ts(od, pa + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kk > 0 || j > 0) ? 1u : 0u);
+            if (s == slots - 1) mma_commit(empty(iv));
+            if (!more) mma_commit(o_full(s));
+          }
+          if (more) {
+            issue_s(s, ik, n16(j + 1));
+            if (lane == 0) {
+              mma_commit(s_full(s));
+              if (j + 2 == w.tiles) mma_commit(q_empty(s));
+              if (s == slots - 1) mma_commit(empty(ik));
+            }
+          }
+        }
+        nk += more ? 2 : 1;
+      }
+    }
+    if (!ok && lane == 0) atomicExch(&abort_sh, 1);
+    // one more commit: its arrival means that every MMA has completed
+    if (lane == 0) {
+      mma_commit(drain);
+      mbar_wait(drain, 0, a.status);
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+// Joins the shares of a row: grid (row tiles, B * Hkv), a warp per row at a time.
+template <int D, bool H>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+  const int t = blockIdx.x, bk = blockIdx.y, lane = threadIdx.x & 31;
+  const int b = bk / a.Hkv, hk = bk % a.Hkv;
+  const int g = t / a.tokens, h = hk * a.G + g;
+  const size_t first = ((size_t)bk * a.pairs + t / 2) * a.splits;    // item of share 0
+  for (int r = threadIdx.x >> 5; r < ROWS; r += 8) {
+    const int n = (t % a.tokens) * ROWS + r;
+    if (n >= a.Nq) break;
+    auto row = [&](int s) { return ((first + s) * SLOTS + (t & 1)) * ROWS + r; };
+    float m = -INFINITY;
+    for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.stat[row(s)].x);
+    m = warp_maxf(m);
+    float l = 0.f, o[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+    if (m > -INFINITY)
+      for (int s = 0; s < a.splits; ++s) {
+        const float2 st = a.stat[row(s)];
+        const float f = exp2f(st.x - m);
+        l += f * st.y;
+        const float* src = a.part + row(s) * D + lane * (D / 32);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
+      }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    char* dst = a.out.data + 2 * (b * a.out.b + h * a.out.h + (int64_t)n * a.out.n) + lane * (D / 16);
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+      *reinterpret_cast<uint32_t*>(dst + 4 * e) = pack2<H>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[((size_t)b * a.Hq + h) * a.Nq + n] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+static void plan(const Problem& p, Args* a) {
+  a->B = p.B; a->Hq = p.Hq; a->Hkv = p.Hkv; a->G = p.G; a->Nq = p.Nq; a->Nk = p.Nk;
+  a->tokens = (p.Nq + ROWS - 1) / ROWS;
+  a->pairs = (p.G * a->tokens + 1) / 2;
+  const int64_t units = (int64_t)p.B * p.Hkv * a->pairs;
+  const int tiles = (p.Nk + KEYS - 1) / KEYS;
+  // shares of the keys: only while that many items still run at once
+  int splits = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, SM_COUNT / std::max<int64_t>(units, 1)));
+  a->splits = splits;
+  a->items = (int)(units * splits);
+}
+
+static size_t workspace(const Problem& p, const Args& a) {
+  return a.splits > 1 ? (size_t)a.items * SLOTS * ROWS * (p.d * sizeof(float) + sizeof(float2)) : 0;
+}
+
+template <int D, bool H>
+static cudaError_t run(const Args& a, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel<D, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  kernel<D, H><<<std::min(a.items, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
+  if (a.splits > 1) join_kernel<D, H><<<dim3(a.G * a.tokens, a.B * a.Hkv), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace many
+
+size_t many_workspace(const Problem& p) {
+  many::Args a = {};
+  many::plan(p, &a);
+  return many::workspace(p, a);
+}
+
+cudaError_t launch_many(const Problem& p, void* ws, cudaStream_t s) {
+  many::Args a = {};
+  many::plan(p, &a);
+  if (!make_tensor_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, p.fp16, many::ROWS) ||
+      !make_tensor_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, p.fp16, many::KEYS) ||
+      !make_tensor_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, p.fp16, many::KEYS))
+    return cudaErrorInvalidValue;
+  a.out = p.out;
+  a.key_len = p.key_len;
+  a.lse = p.lse;
+  a.status = p.status;
+  a.sl2 = p.scale * 1.4426950408889634f;
+  a.wide = ((uintptr_t)p.out.data % 32 == 0 && p.out.b % 16 == 0 && p.out.h % 16 == 0 && p.out.n % 16 == 0);
+  a.part = static_cast<float*>(ws);
+  a.stat = reinterpret_cast<float2*>(a.part + (size_t)a.items * many::SLOTS * many::ROWS * p.d);
+  if (p.d == 128) return p.fp16 ? many::run<128, true>(a, s) : many::run<128, false>(a, s);
+  return p.fp16 ? many::run<64, true>(a, s) : many::run<64, false>(a, s);
+}
+
+}  // namespace cross
+}  // namespace spark
