@@ -37,6 +37,15 @@ struct Packed {
 Packed pack_plan(const Problem& p);
 cudaError_t launch_pack(const Problem& p, const Packed& pk, void* ws, cudaStream_t s);
 
+// Gradients (bf16). p.out is the forward's result; p.key_len counts the kept
+// keys at the front of p.k and p.v; place maps the caller's keys to them (null: itself).
+struct Gradients {
+  View dout, dq, dk, dv;
+  const float* lse;
+};
+size_t bwd_workspace(const Problem& p);
+cudaError_t launch_bwd(const Problem& p, const Gradients& g, const int32_t* place, void* ws, cudaStream_t s);
+
 inline size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 #ifdef __CUDACC__

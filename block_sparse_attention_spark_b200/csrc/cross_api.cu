@@ -39,6 +39,18 @@ static size_t forward_workspace(const Problem& c) {
   return few_rows(c) ? few_workspace(c) : align_up(many_workspace(c)) + pack_plan(c).bytes;
 }
 
+// The problem on the packed copies of its kept keys.
+static cudaError_t pack(Problem* c, char* at, cudaStream_t stream, const int32_t** place) {
+  const Packed pk = pack_plan(*c);
+  const cudaError_t e = launch_pack(*c, pk, at, stream);
+  const int64_t head = (int64_t)c->Nk * c->d;
+  c->k = View{at + pk.off_k, c->Hkv * head, head, c->d};
+  c->v = View{at + pk.off_v, c->Hkv * head, head, c->d};
+  c->key_len = reinterpret_cast<const int32_t*>(at + pk.off_count);
+  if (place) *place = reinterpret_cast<const int32_t*>(at + pk.off_place);
+  return e;
+}
+
 }  // namespace cross
 }  // namespace spark
 
@@ -51,7 +63,7 @@ spark_status spark_cross_validate(const spark_cross_params* p) { return cross::v
 size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd) {
   if (cross::validate(p) != SPARK_OK || (bwd && p->dtype != SPARK_BF16)) return 0;
   const cross::Problem c = cross::problem(p);
-  return cross::forward_workspace(c) + 256;
+  return (bwd ? cross::align_up(cross::bwd_workspace(c)) + cross::pack_plan(c).bytes : cross::forward_workspace(c)) + 256;
 }
 
 spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, const spark_view* k,
@@ -72,23 +84,40 @@ spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, 
   c.lse = lse;
   c.status = device_status();
   if (cross::few_rows(c)) return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
-  if (c.key_mask != nullptr) {
-    char* at = static_cast<char*>(ws) + cross::align_up(cross::many_workspace(c));
-    const cross::Packed pk = cross::pack_plan(c);
-    if (cross::launch_pack(c, pk, at, stream) != cudaSuccess) return SPARK_ERR_CUDA;
-    const int64_t head = (int64_t)c.Nk * c.d;
-    c.k = View{at + pk.off_k, c.Hkv * head, head, c.d};
-    c.v = View{at + pk.off_v, c.Hkv * head, head, c.d};
-    c.key_len = reinterpret_cast<const int32_t*>(at + pk.off_count);
-  }
+  if (c.key_mask != nullptr &&
+      cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::many_workspace(c)), stream, nullptr) != cudaSuccess)
+    return SPARK_ERR_CUDA;
   return cross::launch_many(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
-}  // extern "C"
-
-extern "C" spark_status spark_cross_attn_bwd(const spark_cross_params*, const spark_view*, const spark_view*,
-                                             const spark_view*, const spark_view*, const float*, const spark_view*,
-                                             const int32_t*, const uint8_t*, const spark_view*, const spark_view*,
-                                             const spark_view*, void*, size_t, cudaStream_t) {
-  return SPARK_ERR_UNSUPPORTED;
+spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view* q, const spark_view* k,
+                                  const spark_view* v, const spark_view* out, const float* lse,
+                                  const spark_view* dout, const int32_t* key_len, const uint8_t* key_mask,
+                                  const spark_view* dq, const spark_view* dk, const spark_view* dv, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  const spark_status vs = cross::validate(p);
+  if (vs != SPARK_OK) return vs;
+  if (p->dtype != SPARK_BF16) return SPARK_ERR_UNSUPPORTED;
+  cross::Problem c = cross::problem(p);
+  cross::Gradients g = {};
+  if (!make_view(q, c.B, c.Hq, c.Nq, c.d, 2, false, &c.q) || !make_view(k, c.B, c.Hkv, c.Nk, c.d, 2, false, &c.k) ||
+      !make_view(v, c.B, c.Hkv, c.Nk, c.d, 2, false, &c.v) || !make_view(out, c.B, c.Hq, c.Nq, c.d, 2, false, &c.out) ||
+      !make_view(dout, c.B, c.Hq, c.Nq, c.d, 2, false, &g.dout) ||
+      !make_view(dq, c.B, c.Hq, c.Nq, c.d, 2, true, &g.dq) || !make_view(dk, c.B, c.Hkv, c.Nk, c.d, 2, true, &g.dk) ||
+      !make_view(dv, c.B, c.Hkv, c.Nk, c.d, 2, true, &g.dv))
+    return SPARK_ERR_INVALID_ARG;
+  if (lse == nullptr || ((uintptr_t)lse & 3u) != 0 || ((uintptr_t)key_len & 3u) != 0) return SPARK_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws)) return SPARK_ERR_INVALID_ARG;
+  if (ws_bytes < spark_cross_workspace_size(p, 1)) return SPARK_ERR_WORKSPACE;
+  g.lse = lse;
+  c.key_len = key_len;
+  c.key_mask = key_mask;
+  c.status = device_status();
+  const int32_t* place = nullptr;
+  if (key_mask != nullptr &&
+      cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::bwd_workspace(c)), stream, &place) != cudaSuccess)
+    return SPARK_ERR_CUDA;
+  return cross::launch_bwd(c, g, place, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
+
+}  // extern "C"

@@ -1,0 +1,733 @@
+// Gradient of cross attention on the sm_100a tensor cores (bf16).
+//
+//   D_i = dO_i . O_i,  P = exp(S - lse),  dV = P^T dO,  dS = P (dO V^T - D),
+//   dQ = scale dS K,  dK = scale dS^T Q   (a key head sums over its query heads)
+//
+// Four launches: row_kernel forms D and lse log2 e once; keys_kernel (dK, dV)
+// holds a tile of 128 keys and streams the queries; rows_kernel (dQ) holds a
+// tile of 128 queries and streams the keys; sum_kernel joins the shares of dK
+// and dV. S and dP are formed twice, seven products of 128x128x128 a tile pair
+// where five would do: adding dQ up over key tiles would take float32 atomics
+// (Nk / 128 times Nq d of them, in an order that changes) or one CTA for
+// all the keys.
+//
+// Both kernels: one persistent CTA per SM, eight warps on the elementwise part
+// (each thread one row of the tile's TMEM lanes and half of its 128 columns),
+// one warp on TMA, one on MMAs. P and dS are rounded to bf16 (the operand type
+// of the MMA) and written over their S and dP in TMEM, the lower 64 columns'
+// values at 0..31, the upper ones' at 64..95, so that neither half of the
+// warps writes over what the other half has yet to read; they are the A operand of the
+// second product of each chain. The chains S -> P -> dV and dP -> dS -> dK
+// alternate, so that the tensor cores work on one while the warps work on the other.
+// Products have N = 128 throughout (N = 64 runs at half the rate). Sums, P
+// before rounding and all statistics are float32.
+//
+// Bounded waits as in the forward kernels.
+#include "cross_tc.cuh"
+
+namespace spark {
+namespace cross {
+namespace bwd {
+
+using namespace tc;
+
+constexpr int TILE = 128, EW_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9, THREADS = 320;
+constexpr int STAGES = 5;
+
+struct Args {
+  TensorMap q, k, v, dout;
+  View o, dov, dq, dk, dv;                   // o: out; dov: dout
+  const float* lse;
+  const int32_t* key_len;                    // kept keys per item (after packing), or null
+  const int32_t* place;                      // packed row of each key, or null
+  int* status;
+  int B, Hq, Hkv, G, Nq, Nk, NqP;            // NqP: Nq rounded up to 128
+  int qtiles, ktiles;
+  int ksplits, kper, kitems;                 // shares of a key tile's query tiles, tiles per share
+  int qsplits, qitems;                       // shares of a query tile's key tiles
+  float scale, sl2;
+  float *lse2, *delta;                       // [B * Hq][NqP]
+  float* part;                               // [kitems][2][128][d] shares of dK and dV
+  float* qpart;                              // [qitems][128][d] shares of dQ
+};
+
+// ------------------------------------------------------------------ D and lse
+// One 16-lane (d = 128) or 8-lane (d = 64) group per row: 16 bytes of O and of
+// dO per lane, a shuffle sum. Rows past Nq get lse = +inf (P = 0) and D = 0.
+template <int D>
+__global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ Args a) {
+  constexpr int LPR = D / 8;
+  const int n = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, l = threadIdx.x % LPR;
+  const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
+  if (a.key_len != nullptr && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
+    item_len(a.key_len, a.Nk, b, a.status, true);
+  float s = 0.f;
+  if (n < a.Nq) {
+    const uint4 x = *reinterpret_cast<const uint4*>(a.o.data + 2 * (b * a.o.b + h * a.o.h + (int64_t)n * a.o.n + 8 * l));
+    const uint4 y = *reinterpret_cast<const uint4*>(a.dov.data + 2 * (b * a.dov.b + h * a.dov.h + (int64_t)n * a.dov.n + 8 * l));
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s = fmaf(bf_lo(xs[i]), bf_lo(ys[i]), s);
+      s = fmaf(bf_hi(xs[i]), bf_hi(ys[i]), s);
+    }
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (l == 0 && n < a.NqP) {
+    const size_t at = (size_t)bh * a.NqP + n;
+    a.delta[at] = n < a.Nq ? s : 0.f;
+    a.lse2[at] = n < a.Nq ? a.lse[(size_t)bh * a.Nq + n] * 1.4426950408889634f : INFINITY;
+  }
+}
+
+template <int D>
+struct Lay {
+  static constexpr int ATOMS = D / 64;
+  static constexpr int ATOM = TILE * 128;
+  static constexpr int BYTES = ATOM * ATOMS;           // a tile of 128 rows
+  static constexpr int OFF_ROW = (2 + STAGES) * BYTES; // two slots of lse and D of 128 queries
+  static constexpr int OFF_BAR = OFF_ROW + 2048;
+  static constexpr int SMEM = OFF_BAR + 512;
+  static_assert(SMEM <= 232448, "shared memory of a block");
+};
+constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TILE >> 4) << 24);
+
+// D (TMEM) = A B^T for two tiles of 128 rows (K-major), n of B's rows.
+template <int D>
+__device__ __forceinline__ void product_nt(uint32_t e, uint32_t d, uint32_t sa, uint32_t sb, int n) {
+  const uint64_t da = sdesc(sa, 16, 1024), db = sdesc(sb, 16, 1024);
+  const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint64_t o = (uint64_t)(((ks >> 2) * Lay<D>::ATOM + (ks & 3) * 32) >> 4);
+    mma_f16_if(e, d, da + o, db + o, idesc, ks > 0 ? 1u : 0u);
+  }
+}
+// D (TMEM, 128 x d) (+)= A (TMEM, bf16, 16 rows of B a step) B, B a tile of rows in shared memory.
+template <int D>
+__device__ __forceinline__ void product_ts(uint32_t e, uint32_t d, uint32_t ta, uint32_t sb, int steps, bool add) {
+  const uint64_t db = sdesc(sb, Lay<D>::ATOM, 1024);
+  const uint32_t idesc = IDESC | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+  if (steps == TILE / 16) {
+#pragma unroll
+    for (int kk = 0; kk < TILE / 16; ++kk)
+      mma_ts_if(e, d, ta + 8u * kk + (kk >= 4 ? 32u : 0u), db + (uint64_t)((kk * 2048) >> 4), idesc, (kk > 0 || add) ? 1u : 0u);
+  } else {
+    for (int kk = 0; kk < steps; ++kk)
+      mma_ts_if(e, d, ta + 8u * kk + (kk >= 4 ? 32u : 0u), db + (uint64_t)((kk * 2048) >> 4), idesc, (kk > 0 || add) ? 1u : 0u);
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const TensorMap& m, int n, int h, int b, uint32_t bar) {
+  mbar_arrive_tx(bar, Lay<D>::BYTES);
+#pragma unroll
+  for (int x = 0; x < Lay<D>::ATOMS; ++x)
+    tma_load_4d(dst + x * Lay<D>::ATOM, &m.map, 64 * x, n, m.h_on ? h : 0, m.b_on ? b : 0, bar);
+}
+__device__ __forceinline__ void ew_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Shared start and end of both kernels.
+struct Block {
+  uint32_t base, bar0, tmem;
+  int warp, lane;
+  volatile int* abort_flag;
+};
+template <int D>
+__device__ __forceinline__ bool start(unsigned char* smem, int nbar, const unsigned* counts, int* status, Block& k) {
+  k.lane = threadIdx.x & 31;
+  k.warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+  k.base = smem_u32(smem);
+  if (k.base & 1023u) {                      // the swizzle needs it; the launch guarantees it
+    if (threadIdx.x == 0) set_status(status, STATUS_BAD_INPUT);
+    return false;
+  }
+  k.bar0 = k.base + Lay<D>::OFF_BAR;
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + Lay<D>::OFF_BAR + 8 * nbar);
+  k.abort_flag = reinterpret_cast<volatile int*>(words + 1);
+  if (threadIdx.x == 0) {
+    words[1] = words[2] = 0;             // abort; a wait of the elementwise warps gave up
+    for (int i = 0; i < nbar; ++i) mbar_init(k.bar0 + 8u * i, counts[i]);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (k.warp == MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(words)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  k.tmem = __shfl_sync(0xffffffffu, words[0], 0);
+  return true;
+}
+__device__ __forceinline__ void finish(const Block& k) {
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (k.warp == MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(k.tmem), "r"(512u));
+}
+
+// ------------------------------------------------------------------ dK, dV
+// TMEM: S^T 0, dP^T 128, dV 256, dK 384. Lanes are keys, columns queries.
+// What stands in the rows of k and v past the kept ones only reaches their
+// own lanes, which are not written.
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) keys_kernel(const __grid_constant__ Args a) {
+  using L = Lay<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  enum { FIXED_FULL, FIXED_EMPTY, S_FULL, P_FULL, DP_FULL, DS_FULL, ACC_FULL, ACC_EMPTY, FULL, EMPTY = FULL + STAGES,
+         DRAIN = EMPTY + STAGES, NBAR };
+  unsigned counts[NBAR];
+#pragma unroll
+  for (int i = 0; i < NBAR; ++i) counts[i] = (i == P_FULL || i == DS_FULL || i == ACC_EMPTY) ? EW_WARPS : 1;
+  Block k;
+  if (!start<D>(smem, NBAR, counts, a.status, k)) return;
+  auto bar = [&](int i) { return k.bar0 + 8u * (uint32_t)i; };
+  auto stage = [&](uint32_t i) { return k.base + (2u + i % STAGES) * L::BYTES; };
+  const int L_all = a.G * a.qtiles;          // query tiles of a key head
+  // item: key tile kt of (b, hk), query tiles [t0, t0 + tiles)
+  auto item = [&](int it, int valid, int& b, int& hk, int& kt, int& t0) -> int {
+    const int split = it % a.ksplits, u = it / a.ksplits;
+    kt = u % a.ktiles;
+    hk = u / a.ktiles % a.Hkv;
+    b = u / a.ktiles / a.Hkv;
+    t0 = split * a.kper;
+    return kt * TILE < valid ? max(0, min(a.kper, L_all - t0)) : 0;
+  };
+  auto kept = [&](int it) { return item_len(a.key_len, a.Nk, it / (a.ksplits * a.ktiles * a.Hkv), nullptr, false); };
+
+  if (k.warp < EW_WARPS) {
+    const int half = k.warp >> 2, tid = threadIdx.x;
+    const uint32_t tb = k.tmem + ((uint32_t)((k.warp & 3) * 32) << 16);
+    const uint32_t sc = tb + 64u * (uint32_t)half, dc = tb + 128u + 64u * (uint32_t)half;
+    float* rowsm = reinterpret_cast<float*>(smem + L::OFF_ROW);       // [2][lse 128, D 128]
+    uint32_t nt = 0, ni = 0;                 // tiles, items seen
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
+      int b, hk, kt, t0;
+      const int tiles = item(it, kept(it), b, hk, kt, t0);
+      if (tiles == 0) continue;
+      // this thread's value (lse of column tid, or D of column tid - 128) of a tile
+      auto row_value = [&](int t) {
+        const int h = hk * a.G + t / a.qtiles;
+        const float* src = tid < 128 ? a.lse2 : a.delta;
+        return src[((size_t)b * a.Hq + h) * a.NqP + (t % a.qtiles) * TILE + (tid & 127)];
+      };
+      rowsm[(nt & 1) * 256 + tid] = row_value(t0);
+      ew_sync();
+      for (int j = 0; j < tiles; ++j, ++nt) {
+        const float next = j + 1 < tiles ? row_value(t0 + j + 1) : 0.f;
+        const float4* lse4 = reinterpret_cast<const float4*>(rowsm + (nt & 1) * 256 + 64 * half);
+        const float4* del4 = lse4 + 32;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(S_FULL), nt & 1u, a.status));
+        float p[64];
+        if (ok) {
+          fence_after();
+          uint32_t x[64], pw[32];
+          tmem_ld32p(sc, x);
+          tmem_ld32p(sc + 32u, x + 32);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float4 s = lse4[c];
+            p[4 * c] = ex2(fmaf(__uint_as_float(x[4 * c]), a.sl2, -s.x));
+            p[4 * c + 1] = ex2(fmaf(__uint_as_float(x[4 * c + 1]), a.sl2, -s.y));
+            p[4 * c + 2] = ex2(fmaf(__uint_as_float(x[4 * c + 2]), a.sl2, -s.z));
+            p[4 * c + 3] = ex2(fmaf(__uint_as_float(x[4 * c + 3]), a.sl2, -s.w));
+            pw[2 * c] = pack2<false>(p[4 * c], p[4 * c + 1]);
+            pw[2 * c + 1] = pack2<false>(p[4 * c + 2], p[4 * c + 3]);
+          }
+          tmem_st32p(sc, pw);
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (k.lane == 0) mbar_arrive(bar(P_FULL));
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(DP_FULL), nt & 1u, a.status));
+        }
+        if (ok) {
+          fence_after();
+          uint32_t x[64], w[32];
+          tmem_ld32p(dc, x);
+          tmem_ld32p(dc + 32u, x + 32);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float4 s = del4[c];
+            const float d0 = p[4 * c] * (__uint_as_float(x[4 * c]) - s.x);
+            const float d1 = p[4 * c + 1] * (__uint_as_float(x[4 * c + 1]) - s.y);
+            const float d2 = p[4 * c + 2] * (__uint_as_float(x[4 * c + 2]) - s.z);
+            const float d3 = p[4 * c + 3] * (__uint_as_float(x[4 * c + 3]) - s.w);
+            w[2 * c] = pack2<false>(d0, d1);
+            w[2 * c + 1] = pack2<false>(d2, d3);
+          }
+          tmem_st32p(dc, w);
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (k.lane == 0) mbar_arrive(bar(DS_FULL));
+        }
+        if (j + 1 < tiles) rowsm[((nt + 1) & 1) * 256 + tid] = next;
+        ew_sync();
+      }
+      // shares of dV (the first four warps) and dK
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(ACC_FULL), ni & 1u, a.status));
+      ++ni;
+      if (ok) {
+        fence_after();
+        float* dst = a.part + (((size_t)it * 2 + half) * TILE + (k.warp & 3) * 32 + k.lane) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32p(tb + 256u + 128u * (uint32_t)half + 32u * c, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) store32(dst + 32 * c + e, x + e);
+        }
+        fence_before();
+        __syncwarp();
+        if (k.lane == 0) mbar_arrive(bar(ACC_EMPTY));
+      } else {
+        k.abort_flag[1] = 1;
+      }
+      // the eight warps leave together: they meet at barriers in every item
+      ew_sync();
+      ok = k.abort_flag[1] == 0;
+    }
+    if (!ok) *k.abort_flag = 1;
+  } else if (k.warp == TMA_WARP) {
+    if (k.lane == 0) {
+      uint32_t nf = 0, nk = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
+        int b, hk, kt, t0;
+        const int tiles = item(it, kept(it), b, hk, kt, t0);
+        if (tiles == 0) continue;
+        if (nf > 0) ok = mbar_wait(bar(FIXED_EMPTY), (nf - 1) & 1u, a.status);
+        if (!ok || *k.abort_flag) { ok = false; break; }
+        mbar_arrive_tx(bar(FIXED_FULL), 2 * L::BYTES);
+#pragma unroll
+        for (int x = 0; x < L::ATOMS; ++x) {
+          tma_load_4d(k.base + x * L::ATOM, &a.k.map, 64 * x, kt * TILE, a.k.h_on ? hk : 0, a.k.b_on ? b : 0, bar(FIXED_FULL));
+          tma_load_4d(k.base + L::BYTES + x * L::ATOM, &a.v.map, 64 * x, kt * TILE, a.v.h_on ? hk : 0, a.v.b_on ? b : 0, bar(FIXED_FULL));
+        }
+        ++nf;
+        for (int j = 0; ok && j < 2 * tiles; ++j, ++nk) {
+          // Q_0, dO_0, Q_1, dO_1, ...
+          if (nk >= STAGES) ok = mbar_wait(bar(EMPTY + nk % STAGES), (nk / STAGES - 1) & 1u, a.status);
+          if (!ok || *k.abort_flag) { ok = false; break; }
+          const int t = t0 + (j >> 1);
+          load_tile<D>(stage(nk), (j & 1) ? a.dout : a.q, (t % a.qtiles) * TILE, hk * a.G + t / a.qtiles, b, bar(FULL + nk % STAGES));
+        }
+      }
+      if (nf > 0) mbar_wait(bar(FIXED_FULL), (nf - 1) & 1u, a.status);
+      for (uint32_t x = nk > STAGES ? nk - STAGES : 0; x < nk; ++x) mbar_wait(bar(FULL + x % STAGES), (x / STAGES) & 1u, a.status);
+      if (!ok) *k.abort_flag = 1;
+    }
+  } else {
+    uint32_t nk = 0, nt = 0, ni = 0;
+    const uint32_t e = elect_one();
+    bool ok = true;
+    auto wait = [&](int i, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, a.status));
+      fence_after();
+      return ok;
+    };
+    auto wait_stage = [&](uint32_t i) { return wait(FULL + i % STAGES, (i / STAGES) & 1u); };
+    const uint32_t sK = k.base, sV = k.base + L::BYTES;
+    for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
+      int b, hk, kt, t0;
+      const int tiles = item(it, __shfl_sync(0xffffffffu, kept(it), 0), b, hk, kt, t0);
+      if (tiles == 0) continue;
+      if (!wait(FIXED_FULL, ni & 1u) || !wait_stage(nk)) break;
+      product_nt<D>(e, k.tmem, sK, stage(nk), TILE);
+      mma_commit_if(e, bar(S_FULL));
+      if (!wait_stage(nk + 1)) break;
+      product_nt<D>(e, k.tmem + 128u, sV, stage(nk + 1), TILE);
+      mma_commit_if(e, bar(DP_FULL));
+      for (int j = 0; j < tiles; ++j, ++nt, nk += 2) {
+        const bool more = j + 1 < tiles;
+        if (!wait(P_FULL, nt & 1u)) break;
+        // the accumulators are this item's once the last item's have been read
+        if (j == 0 && ni > 0 && !wait(ACC_EMPTY, (ni - 1) & 1u)) break;
+        product_ts<D>(e, k.tmem + 256u, k.tmem, stage(nk + 1), TILE / 16, j > 0);           // dV += P^T dO
+        mma_commit_if(e, bar(EMPTY + (nk + 1) % STAGES));
+        if (more) {
+          if (!wait_stage(nk + 2)) break;
+          product_nt<D>(e, k.tmem, sK, stage(nk + 2), TILE);
+          mma_commit_if(e, bar(S_FULL));
+        }
+        if (!wait(DS_FULL, nt & 1u)) break;
+        product_ts<D>(e, k.tmem + 384u, k.tmem + 128u, stage(nk), TILE / 16, j > 0);        // dK += dS^T Q
+        mma_commit_if(e, bar(EMPTY + nk % STAGES));
+        if (more) {
+          if (!wait_stage(nk + 3)) break;
+          product_nt<D>(e, k.tmem + 128u, sV, stage(nk + 3), TILE);
+          mma_commit_if(e, bar(DP_FULL));
+        }
+      }
+      if (!ok) break;
+      mma_commit_if(e, bar(FIXED_EMPTY));
+      mma_commit_if(e, bar(ACC_FULL));
+      ++ni;
+    }
+    if (!ok && k.lane == 0) *k.abort_flag = 1;
+    mma_commit_if(e, bar(DRAIN));
+    mbar_wait(bar(DRAIN), 0, a.status);
+    __syncwarp();
+  }
+  finish(k);
+}
+
+// ------------------------------------------------------------------ dQ
+// TMEM: S 0 and 256 (two tiles), dP 128, dQ 384. Lanes are queries, columns keys.
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant__ Args a) {
+  using L = Lay<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  enum { FIXED_FULL, FIXED_EMPTY, S_FULL0, S_FULL1, DP_FULL, DS_FULL, ACC_FULL, ACC_EMPTY, FULL, EMPTY = FULL + STAGES,
+         DRAIN = EMPTY + STAGES, NBAR };
+  unsigned counts[NBAR];
+#pragma unroll
+  for (int i = 0; i < NBAR; ++i) counts[i] = (i == DS_FULL || i == ACC_EMPTY) ? EW_WARPS : 1;
+  Block k;
+  if (!start<D>(smem, NBAR, counts, a.status, k)) return;
+  auto bar = [&](int i) { return k.bar0 + 8u * (uint32_t)i; };
+  auto stage = [&](uint32_t i) { return k.base + (2u + i % STAGES) * L::BYTES; };
+  // item: query tile qt of (b, h), key tiles [k0, k0 + tiles)
+  auto item = [&](int it, int valid, int& b, int& h, int& qt, int& k0) -> int {
+    const int split = it % a.qsplits, u = it / a.qsplits;
+    qt = u % a.qtiles;
+    h = u / a.qtiles % a.Hq;
+    b = u / a.qtiles / a.Hq;
+    const int all = (valid + TILE - 1) / TILE, per = (all + a.qsplits - 1) / a.qsplits;
+    k0 = split * per;
+    return max(0, min(per, all - k0));
+  };
+  auto kept = [&](int it) { return item_len(a.key_len, a.Nk, it / (a.qsplits * a.qtiles * a.Hq), nullptr, false); };
+
+  if (k.warp < EW_WARPS) {
+    const int half = k.warp >> 2, r = (k.warp & 3) * 32 + k.lane;
+    const uint32_t tb = k.tmem + ((uint32_t)((k.warp & 3) * 32) << 16);
+    const uint32_t dc = tb + 128u + 64u * (uint32_t)half;
+    uint32_t nt = 0, ni = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < a.qitems; it += gridDim.x) {
+      int b, h, qt, k0;
+      const int valid = kept(it);
+      const int tiles = item(it, valid, b, h, qt, k0);
+      const size_t at = ((size_t)b * a.Hq + h) * a.NqP + qt * TILE + r;
+      const float lse = a.lse2[at], delta = a.delta[at];
+      for (int j = 0; ok && j < tiles; ++j, ++nt) {
+        const uint32_t sc = tb + 256u * (nt & 1u) + 64u * (uint32_t)half;
+        const int left = valid - (k0 + j) * TILE - 64 * half;        // kept keys among this half's columns
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(S_FULL0 + (nt & 1)), (nt >> 1) & 1u, a.status));
+        if (!ok) break;
+        fence_after();
+        float p[64];
+        {
+          uint32_t x[64];
+          tmem_ld32p(sc, x);
+          tmem_ld32p(sc + 32u, x + 32);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(__uint_as_float(x[c]), a.sl2, -lse));
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(DP_FULL), nt & 1u, a.status));
+        if (!ok) break;
+        fence_after();
+        uint32_t x[64], w[32];
+        tmem_ld32p(dc, x);
+        tmem_ld32p(dc + 32u, x + 32);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(x[c]) - delta;
+        if (left < 64) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c >= left) p[c] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) w[c] = pack2<false>(p[2 * c], p[2 * c + 1]);
+        tmem_st32p(dc, w);
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (k.lane == 0) mbar_arrive(bar(DS_FULL));
+      }
+      if (!ok) break;
+      if (tiles > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(ACC_FULL), ni & 1u, a.status));
+        if (!ok) break;
+        ++ni;
+        fence_after();
+      }
+      // this thread's half of the row's dQ
+      const int n = qt * TILE + r;
+      char* dst = a.dq.data + 2 * (b * a.dq.b + h * a.dq.h + (int64_t)n * a.dq.n + (D / 2) * half);
+      float* share = a.qpart + ((size_t)it * TILE + r) * D + (D / 2) * half;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[32];
+        if (tiles > 0) {
+          tmem_ld32p(tb + 384u + (uint32_t)(D / 2) * half + 32u * c, x);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0u;
+        }
+        if (a.qsplits > 1) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) store32(share + 32 * c + e, x + e);
+        } else if (n < a.Nq) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              w[y] = pack2<false>(__uint_as_float(x[e + 2 * y]) * a.scale, __uint_as_float(x[e + 2 * y + 1]) * a.scale);
+            *reinterpret_cast<uint4*>(dst + 64 * c + 2 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (tiles > 0) {
+        fence_before();
+        __syncwarp();
+        if (k.lane == 0) mbar_arrive(bar(ACC_EMPTY));
+      }
+    }
+    if (!ok) *k.abort_flag = 1;
+  } else if (k.warp == TMA_WARP) {
+    if (k.lane == 0) {
+      uint32_t nf = 0, nk = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; ok && it < a.qitems; it += gridDim.x) {
+        int b, h, qt, k0;
+        const int tiles = item(it, kept(it), b, h, qt, k0);
+        if (tiles == 0) continue;
+        if (nf > 0) ok = mbar_wait(bar(FIXED_EMPTY), (nf - 1) & 1u, a.status);
+        if (!ok || *k.abort_flag) { ok = false; break; }
+        mbar_arrive_tx(bar(FIXED_FULL), 2 * L::BYTES);
+#pragma unroll
+        for (int x = 0; x < L::ATOMS; ++x) {
+          tma_load_4d(k.base + x * L::ATOM, &a.q.map, 64 * x, qt * TILE, a.q.h_on ? h : 0, a.q.b_on ? b : 0, bar(FIXED_FULL));
+          tma_load_4d(k.base + L::BYTES + x * L::ATOM, &a.dout.map, 64 * x, qt * TILE, a.dout.h_on ? h : 0, a.dout.b_on ? b : 0, bar(FIXED_FULL));
+        }
+        ++nf;
+        for (int j = 0; ok && j < 2 * tiles; ++j, ++nk) {
+          // K_0, V_0, K_1, V_1, ...
+          if (nk >= STAGES) ok = mbar_wait(bar(EMPTY + nk % STAGES), (nk / STAGES - 1) & 1u, a.status);
+          if (!ok || *k.abort_flag) { ok = false; break; }
+          load_tile<D>(stage(nk), (j & 1) ? a.v : a.k, (k0 + (j >> 1)) * TILE, h / a.G, b, bar(FULL + nk % STAGES));
+        }
+      }
+      if (nf > 0) mbar_wait(bar(FIXED_FULL), (nf - 1) & 1u, a.status);
+      for (uint32_t x = nk > STAGES ? nk - STAGES : 0; x < nk; ++x) mbar_wait(bar(FULL + x % STAGES), (x / STAGES) & 1u, a.status);
+      if (!ok) *k.abort_flag = 1;
+    }
+  } else {
+    uint32_t nk = 0, nt = 0, ni = 0;
+    const uint32_t e = elect_one();
+    bool ok = true;
+    auto wait = [&](int i, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, a.status));
+      fence_after();
+      return ok;
+    };
+    auto wait_stage = [&](uint32_t i) { return wait(FULL + i % STAGES, (i / STAGES) & 1u); };
+    const uint32_t sQ = k.base, sdO = k.base + L::BYTES;
+    for (int it = blockIdx.x; ok && it < a.qitems; it += gridDim.x) {
+      int b, h, qt, k0;
+      const int valid = __shfl_sync(0xffffffffu, kept(it), 0);
+      const int tiles = item(it, valid, b, h, qt, k0);
+      if (tiles == 0) continue;
+      const int last = valid - (k0 + tiles - 1) * TILE;
+      auto n16 = [&](int j) { return j == tiles - 1 && last < TILE ? (last + 15) & ~15 : TILE; };
+      // S of tile j: K_j's rows past the last kept key are zeroed first, up to
+      // the K of dS K_j (0 * NaN is NaN)
+      auto issue_s = [&](int j) -> bool {
+        const uint32_t i = nk + 2 * (uint32_t)j;
+        if (!wait_stage(i)) return false;
+        const int n = n16(j);
+        if (j == tiles - 1 && n > last) {
+          for (int x = k.lane; x < (n - last) * (D / 8); x += 32) {
+            const int row = last + x / (D / 8), c = x % (D / 8);
+            const uint32_t at = stage(i) + (c >> 3) * L::ATOM + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        product_nt<D>(e, k.tmem + 256u * ((nt + j) & 1u), sQ, stage(i), n);
+        mma_commit_if(e, bar(S_FULL0 + ((nt + j) & 1u)));
+        return true;
+      };
+      auto issue_dp = [&](int j) -> bool {
+        const uint32_t i = nk + 2 * (uint32_t)j + 1;
+        if (!wait_stage(i)) return false;
+        product_nt<D>(e, k.tmem + 128u, sdO, stage(i), n16(j));
+        mma_commit_if(e, bar(DP_FULL));
+        mma_commit_if(e, bar(EMPTY + i % STAGES));
+        return true;
+      };
+      if (!wait(FIXED_FULL, ni & 1u) || !issue_s(0) || !issue_dp(0)) break;
+      if (tiles > 1 && !issue_s(1)) break;
+      for (int j = 0; j < tiles; ++j) {
+        if (!wait(DS_FULL, (nt + j) & 1u)) break;
+        if (j == 0 && ni > 0 && !wait(ACC_EMPTY, (ni - 1) & 1u)) break;
+        product_ts<D>(e, k.tmem + 384u, k.tmem + 128u, stage(nk + 2 * j), n16(j) / 16, j > 0);     // dQ += dS K
+        mma_commit_if(e, bar(EMPTY + (nk + 2 * j) % STAGES));
+        if (j + 1 < tiles && !issue_dp(j + 1)) break;
+        // S buffer (nt + j) & 1 has been read: its P went into dS
+        if (j + 2 < tiles && !issue_s(j + 2)) break;
+      }
+      if (!ok) break;
+      mma_commit_if(e, bar(FIXED_EMPTY));
+      mma_commit_if(e, bar(ACC_FULL));
+      nk += 2 * tiles;
+      nt += tiles;
+      ++ni;
+    }
+    if (!ok && k.lane == 0) *k.abort_flag = 1;
+    mma_commit_if(e, bar(DRAIN));
+    mbar_wait(bar(DRAIN), 0, a.status);
+    __syncwarp();
+  }
+  finish(k);
+}
+
+// ------------------------------------------------------------------ shares
+// dK and dV: shares of a key added in order, eight values a thread. grid
+// (128-key tiles of the caller's keys, Hkv, B), 256 threads.
+template <int D>
+__global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ Args a) {
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int len = item_len(a.key_len, a.Nk, b, nullptr, false);
+  for (int x = threadIdx.x; x < TILE * D / 8; x += 256) {
+    const int n = blockIdx.x * TILE + x / (D / 8), c = 8 * (x % (D / 8));
+    if (n >= a.Nk) break;
+    int row = a.place ? a.place[(size_t)b * a.Nk + n] : n;
+    if (row >= len) row = -1;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      if (row >= 0) {
+        const size_t it = (((size_t)b * a.Hkv + hk) * a.ktiles + row / TILE) * a.ksplits;
+        for (int s = 0; s < a.ksplits; ++s) {
+          const float4* src = reinterpret_cast<const float4*>(a.part + (((it + s) * 2 + y) * TILE + row % TILE) * D + c);
+          const float4 u = src[0], w = src[1];
+          v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
+          v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+        }
+      }
+      const float f = y ? a.scale : 1.f;
+      const View& o = y ? a.dk : a.dv;
+      *reinterpret_cast<uint4*>(o.data + 2 * (b * o.b + hk * o.h + (int64_t)n * o.n + c)) =
+          make_uint4(pack2<false>(v[0] * f, v[1] * f), pack2<false>(v[2] * f, v[3] * f), pack2<false>(v[4] * f, v[5] * f),
+                     pack2<false>(v[6] * f, v[7] * f));
+    }
+  }
+}
+
+// dQ where a query tile's keys were split: grid (query tiles, B * Hq).
+template <int D>
+__global__ void __launch_bounds__(256) sum_rows_kernel(const __grid_constant__ Args a) {
+  const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
+  const size_t it = ((size_t)bh * a.qtiles + blockIdx.x) * a.qsplits;
+  for (int x = threadIdx.x; x < TILE * D / 4; x += 256) {
+    const int r = x / (D / 4), c = 4 * (x % (D / 4)), n = blockIdx.x * TILE + r;
+    if (n >= a.Nq) break;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < a.qsplits; ++s) {
+      const float4 u = *reinterpret_cast<const float4*>(a.qpart + ((it + s) * TILE + r) * D + c);
+      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    }
+    *reinterpret_cast<uint2*>(a.dq.data + 2 * (b * a.dq.b + h * a.dq.h + (int64_t)n * a.dq.n + c)) =
+        make_uint2(pack2<false>(v.x * a.scale, v.y * a.scale), pack2<false>(v.z * a.scale, v.w * a.scale));
+  }
+}
+
+struct Plan {
+  size_t off_lse, off_delta, off_part, off_qpart, bytes;
+};
+
+static Plan plan(const Problem& p, Args* a) {
+  a->B = p.B; a->Hq = p.Hq; a->Hkv = p.Hkv; a->G = p.G; a->Nq = p.Nq; a->Nk = p.Nk;
+  a->qtiles = (p.Nq + TILE - 1) / TILE;
+  a->ktiles = (p.Nk + TILE - 1) / TILE;
+  a->NqP = a->qtiles * TILE;
+  // shares of a key tile's queries: the fewest of those that leave the SMs
+  // within 2% of the least time (rounds of items times tiles an item, and about a
+  // tile's time for each item's start, end and its part of the sums)
+  const int64_t units = (int64_t)p.B * p.Hkv * a->ktiles;
+  const int64_t L = (int64_t)p.G * a->qtiles;
+  auto cost = [&](int64_t s) { return (units * s + SM_COUNT - 1) / SM_COUNT * ((L + s - 1) / s + 1); };
+  const int64_t most = std::min<int64_t>(L, std::max<int64_t>(1, 12 * SM_COUNT / std::max<int64_t>(units, 12)));
+  int64_t least = cost(1);
+  for (int64_t s = 2; s <= most; ++s) least = std::min(least, cost(s));
+  int64_t ks = 1;
+  while (cost(ks) * 100 > least * 102) ++ks;
+  a->kper = (int)((L + ks - 1) / ks);
+  a->ksplits = (int)((L + a->kper - 1) / a->kper);
+  a->kitems = (int)(units * a->ksplits);
+  const int64_t rows = (int64_t)p.B * p.Hq * a->qtiles;
+  a->qsplits = (int)std::max<int64_t>(1, std::min<int64_t>(a->ktiles, SM_COUNT / rows));
+  a->qitems = (int)(rows * a->qsplits);
+  Plan pl;
+  size_t o = 0;
+  auto take = [&](size_t n) { const size_t at = o; o = align_up(o + n); return at; };
+  pl.off_lse = take((size_t)p.B * p.Hq * a->NqP * 4);
+  pl.off_delta = take((size_t)p.B * p.Hq * a->NqP * 4);
+  pl.off_part = take((size_t)a->kitems * 2 * TILE * p.d * 4);
+  pl.off_qpart = take(a->qsplits > 1 ? (size_t)a->qitems * TILE * p.d * 4 : 0);
+  pl.bytes = o;
+  return pl;
+}
+
+template <int D>
+static cudaError_t run(const Args& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(keys_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  row_kernel<D><<<dim3(a.NqP / (256 / (D / 8)), a.B * a.Hq), 256, 0, s>>>(a);
+  keys_kernel<D><<<std::min(a.kitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
+  rows_kernel<D><<<std::min(a.qitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
+  sum_kernel<D><<<dim3(a.ktiles, a.Hkv, a.B), 256, 0, s>>>(a);
+  if (a.qsplits > 1) sum_rows_kernel<D><<<dim3(a.qtiles, a.B * a.Hq), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace bwd
+
+size_t bwd_workspace(const Problem& p) {
+  bwd::Args a = {};
+  return bwd::plan(p, &a).bytes;
+}
+
+cudaError_t launch_bwd(const Problem& p, const Gradients& g, const int32_t* place, void* ws, cudaStream_t s) {
+  bwd::Args a = {};
+  const bwd::Plan pl = bwd::plan(p, &a);
+  if (!make_tensor_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE) ||
+      !make_tensor_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
+      !make_tensor_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
+      !make_tensor_map(&a.dout, g.dout, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE))
+    return cudaErrorInvalidValue;
+  char* w = static_cast<char*>(ws);
+  a.o = p.out; a.dov = g.dout; a.dq = g.dq; a.dk = g.dk; a.dv = g.dv;
+  a.lse = g.lse;
+  a.key_len = p.key_len;
+  a.place = place;
+  a.status = p.status;
+  a.scale = p.scale;
+  a.sl2 = p.scale * 1.4426950408889634f;
+  a.lse2 = reinterpret_cast<float*>(w + pl.off_lse);
+  a.delta = reinterpret_cast<float*>(w + pl.off_delta);
+  a.part = reinterpret_cast<float*>(w + pl.off_part);
+  a.qpart = reinterpret_cast<float*>(w + pl.off_qpart);
+  return p.d == 128 ? bwd::run<128>(a, s) : bwd::run<64>(a, s);
+}
+
+}  // namespace cross
+}  // namespace spark

@@ -31,8 +31,7 @@
 
 #include "common.cuh"
 #include "cross.h"
-#include "tc_ptx.cuh"
-#include "tma_map.h"
+#include "cross_tc.cuh"
 
 namespace spark {
 namespace cross {
@@ -76,70 +75,27 @@ struct Lay {
   static constexpr int SMEM = (SLOTS + STAGES) * TILE + 1024;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int n, int h, int b,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(n), "r"(h), "r"(b), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-template <bool H>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if constexpr (H) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // A work item: its key head, its share of the keys and the two row tiles.
 struct Item {
   int b, hk, pair, k0, valid, tiles;         // first key tile, kept keys of the item, key tiles of the share
 };
-__device__ __forceinline__ Item item_of(const Args& a, int it) {
+__device__ __forceinline__ int item_batch(const Args& a, int it) { return it / (a.splits * a.pairs * a.Hkv); }
+__device__ __forceinline__ Item item_of(const Args& a, int it, int valid) {
   Item w;
   const int split = it % a.splits, u = it / a.splits;
   w.pair = u % a.pairs;
   const int bk = u / a.pairs;
   w.b = bk / a.Hkv;
   w.hk = bk % a.Hkv;
-  w.valid = item_len(a.key_len, a.Nk, w.b, nullptr, false);
+  w.valid = valid;
   const int all = (w.valid + KEYS - 1) / KEYS, per = (all + a.splits - 1) / a.splits;
   w.k0 = split * per;
   w.tiles = max(0, min(per, all - w.k0));
   return w;
+}
+
+__device__ __forceinline__ int kept(const Args& a, int it) {
+  return item_len(a.key_len, a.Nk, item_batch(a, it), nullptr, false);
 }
 
 template <int D, bool H>
@@ -154,7 +110,8 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // uniform
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_u32(&bars[0]);
   auto q_full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
@@ -182,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_sh;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
   const int row_tiles = a.G * a.tokens;
 
   if (warp < SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
@@ -198,7 +155,7 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
     if (a.key_len != nullptr && blockIdx.x == 0 && s == 0)
       for (int b = r; b < a.B; b += ROWS) item_len(a.key_len, a.Nk, b, a.status, true);
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item w = item_of(a, it);
+      const Item w = item_of(a, it, kept(a, it));
       const int t = 2 * w.pair + s;
       if (t >= row_tiles) continue;
       float m = -INFINITY, l = 0.f;
@@ -344,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
       uint32_t nk = 0, nq[SLOTS] = {0, 0};   // tiles issued
       bool ok = true;
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-        const Item w = item_of(a, it);
+        const Item w = item_of(a, it, kept(a, it));
         if (w.tiles == 0) continue;
         for (int s = 0; ok && s < SLOTS; ++s) {
           const int t = 2 * w.pair + s;
@@ -379,8 +336,9 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
       if (!ok) atomicExch(&abort_sh, 1);
     }
   } else if (warp == MMA_WARP) {
-    // ------------------------------------------------ MMAs (all lanes wait, lane 0 issues)
+    // ------------------------------------------------ MMAs (warp-uniform, one lane's predicate on)
     uint32_t nk = 0, nq[SLOTS] = {0, 0}, np[SLOTS] = {0, 0};
+    const uint32_t e = elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status));
@@ -389,17 +347,16 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
     };
     // S of a slot from K in stage i, n keys (a multiple of 16)
     auto issue_s = [&](int s, int i, int n) {
-      if (lane != 0) return;
       const uint64_t dq = sdesc(sQ(s), 16, 1024), dk = sdesc(sKV(i), 16, 1024);
       const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint64_t o = (uint64_t)(((ks >> 2) * L::ATOM + (ks & 3) * 32) >> 4);
-        mma_f16(tmem + 128u * (uint32_t)s, dq + o, dk + o, idesc, ks > 0 ? 1u : 0u);
+        mma_f16_if(e, tmem + 128u * (uint32_t)s, dq + o, dk + o, idesc, ks > 0 ? 1u : 0u);
       }
     };
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
-      const Item w = item_of(a, it);
+      const Item w = item_of(a, it, __shfl_sync(0xffffffffu, kept(a, it), 0));
       if (w.tiles == 0) continue;
       const int slots = 2 * w.pair + 1 < row_tiles ? 2 : 1;
       const int last = w.valid - (w.k0 + w.tiles - 1) * KEYS;       // keys of the last tile
@@ -409,11 +366,9 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         if (!wait(q_full(s), nq[s] & 1u)) break;
         ++nq[s];
         issue_s(s, nk % L::STAGES, n16(0));
-        if (lane == 0) {
-          mma_commit(s_full(s));
-          if (w.tiles == 1) mma_commit(q_empty(s));
-          if (s == slots - 1) mma_commit(empty(nk % L::STAGES));
-        }
+        mma_commit_if(e, s_full(s));
+        if (w.tiles == 1) mma_commit_if(e, q_empty(s));
+        if (s == slots - 1) mma_commit_if(e, empty(nk % L::STAGES));
       }
       ++nk;
       for (int j = 0; ok && j < w.tiles; ++j) {
@@ -424,8 +379,8 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         const int n = n16(j);
         if (!more && (last & 15) != 0) {
           // rows of V past the last kept key, up to the MMA's K
-          for (int e = lane; e < (n - last) * (D / 8); e += 32) {
-            const int row = last + e / (D / 8), c = e % (D / 8);
+          for (int x = lane; x < (n - last) * (D / 8); x += 32) {
+            const int row = last + x / (D / 8), c = x % (D / 8);
             const uint32_t at = sKV(iv) + (c >> 3) * L::ATOM + row * 128 + (((c & 7) ^ (row & 7)) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
           }
@@ -436,21 +391,24 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         for (int s = 0; ok && s < slots; ++s) {
           if (!wait(p_full(s), np[s] & 1u)) break;
           ++np[s];
-          if (lane == 0) {
-            const uint64_t dv = sdesc(sKV(iv), L::ATOM, 1024);
-            const uint32_t pa = tmem + 128u * (uint32_t)s, od = tmem + O_COL + 128u * (uint32_t)s;
+          const uint64_t dv = sdesc(sKV(iv), L::ATOM, 1024);
+          const uint32_t pa = tmem + 128u * (uint32_t)s, od = tmem + O_COL + 128u * (uint32_t)s;
+          if (n == KEYS) {
+#pragma unroll
+            for (int kk = 0; kk < KEYS / 16; ++kk)
+              mma_ts_if(e, od, pa + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kk > 0 || j > 0) ? 1u : 0u);
+          } else {
             for (int kk = 0; kk < n / 16; ++kk)
-              mma_ts(od, pa + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kk > 0 || j > 0) ? 1u : 0u);
-            if (s == slots - 1) mma_commit(empty(iv));
-            if (!more) mma_commit(o_full(s));
+              mma_ts_if(e, od, pa + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kk > 0 || j > 0) ? 1u : 0u);
           }
-          if (more) {
+          if (s == slots - 1) mma_commit_if(e, empty(iv));
+          if (!more) {
+            mma_commit_if(e, o_full(s));
+          } else {
             issue_s(s, ik, n16(j + 1));
-            if (lane == 0) {
-              mma_commit(s_full(s));
-              if (j + 2 == w.tiles) mma_commit(q_empty(s));
-              if (s == slots - 1) mma_commit(empty(ik));
-            }
+            mma_commit_if(e, s_full(s));
+            if (j + 2 == w.tiles) mma_commit_if(e, q_empty(s));
+            if (s == slots - 1) mma_commit_if(e, empty(ik));
           }
         }
         nk += more ? 2 : 1;
@@ -458,10 +416,8 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
     }
     if (!ok && lane == 0) atomicExch(&abort_sh, 1);
     // one more commit: its arrival means that every MMA has completed
-    if (lane == 0) {
-      mma_commit(drain);
-      mbar_wait(drain, 0, a.status);
-    }
+    mma_commit_if(e, drain);
+    mbar_wait(drain, 0, a.status);
     __syncwarp();
   }
   fence_before();
