@@ -597,56 +597,50 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ shares
-// dK and dV: shares of a key added in order, eight values a thread. grid
-// (128-key tiles of the caller's keys, Hkv, B), 256 threads.
+// dK and dV: shares of a key added in order, eight values a thread; the lower
+// 128 threads of a block dV, the upper ones dK. grid (keys / (1024 / d), Hkv, B).
 template <int D>
 __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ Args a) {
-  const int hk = blockIdx.y, b = blockIdx.z;
-  const int len = item_len(a.key_len, a.Nk, b, nullptr, false);
-  for (int x = threadIdx.x; x < TILE * D / 8; x += 256) {
-    const int n = blockIdx.x * TILE + x / (D / 8), c = 8 * (x % (D / 8));
-    if (n >= a.Nk) break;
-    int row = a.place ? a.place[(size_t)b * a.Nk + n] : n;
-    if (row >= len) row = -1;
+  const int hk = blockIdx.y, b = blockIdx.z, y = threadIdx.x >> 7, x = threadIdx.x & 127;
+  const int n = blockIdx.x * (1024 / D) + x / (D / 8), c = 8 * (x % (D / 8));
+  if (n >= a.Nk) return;
+  int row = a.place ? a.place[(size_t)b * a.Nk + n] : n;
+  if (row >= item_len(a.key_len, a.Nk, b, nullptr, false)) row = -1;
+  float v[8];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      if (row >= 0) {
-        const size_t it = (((size_t)b * a.Hkv + hk) * a.ktiles + row / TILE) * a.ksplits;
-        for (int s = 0; s < a.ksplits; ++s) {
-          const float4* src = reinterpret_cast<const float4*>(a.part + (((it + s) * 2 + y) * TILE + row % TILE) * D + c);
-          const float4 u = src[0], w = src[1];
-          v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
-          v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
-        }
-      }
-      const float f = y ? a.scale : 1.f;
-      const View& o = y ? a.dk : a.dv;
-      *reinterpret_cast<uint4*>(o.data + 2 * (b * o.b + hk * o.h + (int64_t)n * o.n + c)) =
-          make_uint4(pack2<false>(v[0] * f, v[1] * f), pack2<false>(v[2] * f, v[3] * f), pack2<false>(v[4] * f, v[5] * f),
-                     pack2<false>(v[6] * f, v[7] * f));
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if (row >= 0) {
+    const size_t it = (((size_t)b * a.Hkv + hk) * a.ktiles + row / TILE) * a.ksplits;
+#pragma unroll 4
+    for (int s = 0; s < a.ksplits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(a.part + (((it + s) * 2 + y) * TILE + row % TILE) * D + c);
+      const float4 u = src[0], w = src[1];
+      v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
+      v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
     }
   }
+  const float f = y ? a.scale : 1.f;
+  const View& o = y ? a.dk : a.dv;
+  *reinterpret_cast<uint4*>(o.data + 2 * (b * o.b + hk * o.h + (int64_t)n * o.n + c)) =
+      make_uint4(pack2<false>(v[0] * f, v[1] * f), pack2<false>(v[2] * f, v[3] * f), pack2<false>(v[4] * f, v[5] * f),
+                 pack2<false>(v[6] * f, v[7] * f));
 }
 
-// dQ where a query tile's keys were split: grid (query tiles, B * Hq).
+// dQ where a query tile's keys were split: four values a thread. grid (queries / (1024 / d), B * Hq).
 template <int D>
 __global__ void __launch_bounds__(256) sum_rows_kernel(const __grid_constant__ Args a) {
   const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
-  const size_t it = ((size_t)bh * a.qtiles + blockIdx.x) * a.qsplits;
-  for (int x = threadIdx.x; x < TILE * D / 4; x += 256) {
-    const int r = x / (D / 4), c = 4 * (x % (D / 4)), n = blockIdx.x * TILE + r;
-    if (n >= a.Nq) break;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < a.qsplits; ++s) {
-      const float4 u = *reinterpret_cast<const float4*>(a.qpart + ((it + s) * TILE + r) * D + c);
-      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-    }
-    *reinterpret_cast<uint2*>(a.dq.data + 2 * (b * a.dq.b + h * a.dq.h + (int64_t)n * a.dq.n + c)) =
-        make_uint2(pack2<false>(v.x * a.scale, v.y * a.scale), pack2<false>(v.z * a.scale, v.w * a.scale));
+  const int n = blockIdx.x * (1024 / D) + threadIdx.x / (D / 4), c = 4 * (threadIdx.x % (D / 4));
+  if (n >= a.Nq) return;
+  const size_t it = ((size_t)bh * a.qtiles + n / TILE) * a.qsplits;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < a.qsplits; ++s) {
+    const float4 u = *reinterpret_cast<const float4*>(a.qpart + ((it + s) * TILE + n % TILE) * D + c);
+    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
   }
+  *reinterpret_cast<uint2*>(a.dq.data + 2 * (b * a.dq.b + h * a.dq.h + (int64_t)n * a.dq.n + c)) =
+      make_uint2(pack2<false>(v.x * a.scale, v.y * a.scale), pack2<false>(v.z * a.scale, v.w * a.scale));
 }
 
 struct Plan {
@@ -694,8 +688,8 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
   row_kernel<D><<<dim3(a.NqP / (256 / (D / 8)), a.B * a.Hq), 256, 0, s>>>(a);
   keys_kernel<D><<<std::min(a.kitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
   rows_kernel<D><<<std::min(a.qitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
-  sum_kernel<D><<<dim3(a.ktiles, a.Hkv, a.B), 256, 0, s>>>(a);
-  if (a.qsplits > 1) sum_rows_kernel<D><<<dim3(a.qtiles, a.B * a.Hq), 256, 0, s>>>(a);
+  sum_kernel<D><<<dim3((a.Nk * (D / 64) + 15) / 16, a.Hkv, a.B), 256, 0, s>>>(a);
+  if (a.qsplits > 1) sum_rows_kernel<D><<<dim3((a.Nq * (D / 64) + 15) / 16, a.B * a.Hq), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -40,12 +40,14 @@ namespace many {
 using namespace tc;
 
 constexpr int ROWS = 128, KEYS = 128, SLOTS = 2;
-constexpr int SM_WARPS = 4 * SLOTS, TMA_WARP = SM_WARPS, MMA_WARP = SM_WARPS + 1;
-constexpr int THREADS = 32 * (SM_WARPS + 4);      // two warps of the last group stay idle
-// A thread is launched with 168 registers (three warps per scheduler); the
-// softmax needs about 200, the other group little: 256 * 208 + 128 * 88 = 384 * 168.
-constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 208, OTHER_REGS = 88;
-static_assert(SM_WARPS * 32 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * LAUNCH_REGS, "registers the block owns");
+// warps: softmax of tile 0 and of tile 1 (four each), TMA, MMA, two idle, output (four)
+constexpr int SM_WARPS = 4 * SLOTS, TMA_WARP = SM_WARPS, MMA_WARP = SM_WARPS + 1, OUT_WARP0 = SM_WARPS + 4;
+constexpr int THREADS = 32 * (SM_WARPS + 8);
+// A thread is launched with 128 registers; the softmax needs about 180, the
+// others little: 256 * 184 + 256 * 72 = 512 * 128.
+constexpr int LAUNCH_REGS = 128, SOFTMAX_REGS = 184, OTHER_REGS = 72;
+static_assert(SM_WARPS * 32 * SOFTMAX_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS, "registers the block owns");
+constexpr int QBUFS = 3;                     // a row tile's Q can load while both current ones are in use
 constexpr float LAZY = 8.0f;                 // log2 units
 constexpr uint32_t O_COL = 256;
 
@@ -71,8 +73,11 @@ struct Lay {
   static constexpr int ATOMS = D / 64;
   static constexpr int ATOM = 128 * 128;               // 128 rows x 64 values
   static constexpr int TILE = ATOM * ATOMS;            // Q tile = K tile = V tile
-  static constexpr int STAGES = 5;
-  static constexpr int SMEM = (SLOTS + STAGES) * TILE + 1024;
+  static constexpr int STAGES = D == 128 ? 4 : 8;      // of K and V
+  static constexpr int OFF_STAT = (QBUFS + STAGES) * TILE;   // (reference, sum) of both tiles' rows
+  static constexpr int OFF_BAR = OFF_STAT + SLOTS * ROWS * 8;
+  static constexpr int SMEM = OFF_BAR + 512;
+  static_assert(SMEM <= 232448, "shared memory of a block");
 };
 
 // A work item: its key head, its share of the keys and the two row tiles.
@@ -101,45 +106,53 @@ __device__ __forceinline__ int kept(const Args& a, int it) {
 template <int D, bool H>
 __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Args a) {
   using L = Lay<D>;
-  constexpr int NBAR = 10 + 2 * L::STAGES + 1;
+  enum { S_FULL = 0, P_FULL = 2, O_FULL = 6, O_EMPTY = 8, L_FULL = 10, L_EMPTY = 12, Q_FULL = 14, Q_EMPTY = Q_FULL + QBUFS,
+         FULL = Q_EMPTY + QBUFS, EMPTY = FULL + L::STAGES, DRAIN = EMPTY + L::STAGES, NBAR };
   constexpr uint32_t FMT = H ? 0u : 1u;
   constexpr uint32_t IDESC = (1u << 4) | (FMT << 7) | (FMT << 10) | ((uint32_t)(ROWS >> 4) << 24);
   constexpr uint32_t IDESC_O = IDESC | (1u << 16) | ((uint32_t)(D >> 3) << 17);
-  extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[NBAR];
-  __shared__ uint32_t tmem_sh;
-  __shared__ int abort_sh;
+  static_assert(8 * NBAR + 8 <= 512, "barriers");
+  extern __shared__ __align__(1024) unsigned char smem[];
+  float2* stat_sh = reinterpret_cast<float2*>(smem + L::OFF_STAT);       // [SLOTS][ROWS]
+  uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + 8 * NBAR);
+  int& abort_sh = *reinterpret_cast<int*>(tmem_sh + 1);
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // uniform
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t bar0 = smem_u32(&bars[0]);
-  auto q_full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
-  auto q_empty = [&](int s) { return bar0 + 8u * (uint32_t)(2 + s); };
-  auto s_full = [&](int s) { return bar0 + 8u * (uint32_t)(4 + s); };
-  auto p_full = [&](int s) { return bar0 + 8u * (uint32_t)(6 + s); };
-  // O has a barrier of its own: the next item's first S may arrive before the
-  // warps have looked at this one's O, and a parity wait must not fall two phases behind
-  auto o_full = [&](int s) { return bar0 + 8u * (uint32_t)(8 + s); };
-  auto full = [&](int i) { return bar0 + 8u * (uint32_t)(10 + i); };
-  auto empty = [&](int i) { return bar0 + 8u * (uint32_t)(10 + L::STAGES + i); };
-  const uint32_t drain = bar0 + 8u * (uint32_t)(10 + 2 * L::STAGES);
-  auto sQ = [&](int s) { return base + (uint32_t)(s * L::TILE); };
-  auto sKV = [&](int i) { return base + (uint32_t)((SLOTS + i) * L::TILE); };
+  const uint32_t base = smem_u32(smem), bar0 = base + L::OFF_BAR;
+  if (base & 1023u) {                        // the swizzle needs it; the launch guarantees it
+    if (tid == 0) set_status(a.status, STATUS_BAD_INPUT);
+    return;
+  }
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  // O has barriers of its own: the next item's first S may arrive before this one's
+  // O has been looked at, and a parity wait must not fall two phases behind
+  auto s_full = [&](int s) { return bar(S_FULL + s); };
+  auto p_full = [&](int s, int half) { return bar(P_FULL + 2 * s + half); };   // P of the lower, the upper 64 keys
+  auto o_full = [&](int s) { return bar(O_FULL + s); };
+  auto o_empty = [&](int s) { return bar(O_EMPTY + s); };
+  auto l_full = [&](int s) { return bar(L_FULL + s); };
+  auto l_empty = [&](int s) { return bar(L_EMPTY + s); };
+  auto q_full = [&](uint32_t x) { return bar(Q_FULL + x % QBUFS); };
+  auto q_empty = [&](uint32_t x) { return bar(Q_EMPTY + x % QBUFS); };
+  auto full = [&](uint32_t x) { return bar(FULL + x % L::STAGES); };
+  auto empty = [&](uint32_t x) { return bar(EMPTY + x % L::STAGES); };
+  auto sQ = [&](uint32_t x) { return base + (x % QBUFS) * L::TILE; };
+  auto sKV = [&](uint32_t x) { return base + (QBUFS + x % L::STAGES) * L::TILE; };
 
   if (tid == 0) {
     abort_sh = 0;
-    for (int i = 0; i < NBAR; ++i) mbar_init(bar0 + 8u * i, (i == 6 || i == 7) ? 4 : 1);
+    for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), (i >= P_FULL && i < O_FULL) || (i >= O_EMPTY && i < Q_FULL) ? 4 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == MMA_WARP) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_sh)), "r"(512u));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_sh)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_sh, 0);
   const int row_tiles = a.G * a.tokens;
 
   if (warp < SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
@@ -150,14 +163,13 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
     const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t sc = tb + 128u * (uint32_t)s, oc = tb + O_COL + 128u * (uint32_t)s;
     const uint64_t sc2 = f2(a.sl2, a.sl2);
-    uint32_t ns = 0, no = 0;                 // S tiles and O's seen
+    uint32_t ns = 0, ni = 0;                 // S tiles, items seen
     bool ok = true;
     if (a.key_len != nullptr && blockIdx.x == 0 && s == 0)
       for (int b = r; b < a.B; b += ROWS) item_len(a.key_len, a.Nk, b, a.status, true);
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
       const Item w = item_of(a, it, kept(a, it));
-      const int t = 2 * w.pair + s;
-      if (t >= row_tiles) continue;
+      if (w.tiles == 0 || 2 * w.pair + s >= row_tiles) continue;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; ok && j < w.tiles; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait(s_full(s), ns & 1u, a.status));
@@ -216,36 +228,64 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
           for (int c = 0; c < 64; c += 2) {
             float u0, u1;
             unf2(ffma2(f2(__uint_as_float(sv[64 * hf + c]), __uint_as_float(sv[64 * hf + c + 1])), sc2, nm2), u0, u1);
-            const float p0 = ex2(u0), p1 = ex2(u1);
-            acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], f2(p0, p1));
-            pw[c >> 1] = pack2<H>(p0, p1);
+            u0 = ex2(u0);
+            u1 = ex2(u1);
+            acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], f2(u0, u1));
+            pw[c >> 1] = pack2<H>(u0, u1);
           }
           tmem_st32p(sc + 32u * hf, pw);
+          // the MMAs of these 64 keys need not wait for the others
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(s, hf));
         }
         float r0, r1, r2, r3;
         unf2(fadd2(acc[0], acc[1]), r0, r1);
         unf2(fadd2(acc[2], acc[3]), r2, r3);
-        const float rs = (r0 + r2) + (r1 + r3);
-        l = l * corr + rs;
+        l = l * corr + ((r0 + r2) + (r1 + r3));
         m = m_new;
-        tmem_st_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(s));
       }
       if (!ok) break;
-      // ---- O of this row tile
-      if (w.tiles > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(o_full(s), no & 1u, a.status));
-        ++no;
-        if (!ok) break;
-        fence_after();
-      }
-      const int g = t / a.tokens, n = (t % a.tokens) * ROWS + r;
-      const bool live = n < a.Nq;
-      const int h = w.hk * a.G + g;
-      if (a.splits > 1) {
-        float* dst = a.part + ((size_t)it * SLOTS + s) * ROWS * D + (size_t)r * D;
+      // for the output warps, once they have the last item's
+      if (ni > 0) ok = __all_sync(0xffffffffu, mbar_wait(l_empty(s), (ni - 1) & 1u, a.status));
+      if (!ok) break;
+      stat_sh[s * ROWS + r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(l_full(s));
+      ++ni;
+    }
+    if (!ok) atomicExch(&abort_sh, 1);
+  } else if (warp >= OUT_WARP0) {
+    // ------------------------------------------------ output: O of each row tile while the softmax is at the next item
+    const int r = (warp - OUT_WARP0) * 32 + lane;
+    const uint32_t tb = tmem + ((uint32_t)((warp - OUT_WARP0) * 32) << 16);
+    uint32_t ni[SLOTS] = {0, 0};
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
+      const Item w = item_of(a, it, kept(a, it));
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        const int t = 2 * w.pair + s;
+        if (!ok || t >= row_tiles) break;
+        float m = -INFINITY, l = 0.f;
+        if (w.tiles > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(l_full(s), ni[s] & 1u, a.status) && mbar_wait(o_full(s), ni[s] & 1u, a.status));
+          if (!ok) break;
+          fence_after();
+          const float2 st = stat_sh[s * ROWS + r];
+          m = st.x;
+          l = st.y;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(l_empty(s));
+          ++ni[s];
+        }
+        const uint32_t oc = tb + O_COL + 128u * (uint32_t)s;
+        const int g = t / a.tokens, n = (t % a.tokens) * ROWS + r, h = w.hk * a.G + g;
+        const bool live = n < a.Nq;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        float* part = a.part + ((size_t)it * SLOTS + s) * ROWS * D + (size_t)r * D;
+        char* dst = a.out.data + 2 * (w.b * a.out.b + h * a.out.h + (int64_t)n * a.out.n);
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
@@ -256,29 +296,21 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
-          if (live) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) store32(dst + 32 * cc + e, o + e);
+          if (cc == D / 32 - 1 && w.tiles > 0) {           // O has been read
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_empty(s));
           }
-        }
-        if (live) a.stat[((size_t)it * SLOTS + s) * ROWS + r] = make_float2(m, l);
-      } else {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        char* dst = a.out.data + 2 * (w.b * a.out.b + h * a.out.h + (int64_t)n * a.out.n);
-#pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t o[32], pk[16];
-          if (w.tiles > 0) {
-            tmem_ld32p(oc + 32u * cc, o);
-            tmem_ld_wait();
-          } else {
+          if (a.splits > 1) {
+            if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
-          }
+              for (int e = 0; e < 32; e += 8) store32(part + 32 * cc + e, o + e);
+            }
+          } else if (live) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            pk[e] = pack2<H>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          if (live) {
+            for (int e = 0; e < 16; ++e)
+              pk[e] = pack2<H>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
             if (a.wide) {
               store32(dst + 64 * cc, pk);
               store32(dst + 64 * cc + 32, pk + 8);
@@ -289,55 +321,50 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
             }
           }
         }
-        if (live && a.lse != nullptr)
+        if (live && a.splits > 1) a.stat[((size_t)it * SLOTS + s) * ROWS + r] = make_float2(m, l);
+        if (live && a.splits == 1 && a.lse != nullptr)
           a.lse[((size_t)w.b * a.Hq + h) * a.Nq + n] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
-      fence_before();                        // O has been read: ordered before the next P's arrival
     }
     if (!ok) atomicExch(&abort_sh, 1);
   } else if (warp == TMA_WARP) {
-    // ------------------------------------------------ loads: Q of both tiles, K_0, V_0, K_1, V_1, ...
+    // ------------------------------------------------ loads: Q of tile 0, K_0, Q of tile 1, V_0, K_1, V_1, ...
     if (lane == 0) {
-      uint32_t nk = 0, nq[SLOTS] = {0, 0};   // tiles issued
+      uint32_t nk = 0, nq = 0;               // tiles issued
       bool ok = true;
+      auto load = [&](uint32_t dst, const TensorMap& m, int n, int h, int b, uint32_t full_bar, uint32_t empty_bar,
+                      bool used, uint32_t parity) {
+        if (used) ok = mbar_wait(empty_bar, parity, a.status);
+        if (!ok || *(volatile int*)&abort_sh) { ok = false; return; }
+        mbar_arrive_tx(full_bar, L::TILE);
+#pragma unroll
+        for (int x = 0; x < L::ATOMS; ++x)
+          tma_load_4d(dst + x * L::ATOM, &m.map, 64 * x, n, m.h_on ? h : 0, m.b_on ? b : 0, full_bar);
+      };
       for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
         const Item w = item_of(a, it, kept(a, it));
-        if (w.tiles == 0) continue;
-        for (int s = 0; ok && s < SLOTS; ++s) {
-          const int t = 2 * w.pair + s;
-          if (t >= row_tiles) continue;
-          if (nq[s] > 0) ok = mbar_wait(q_empty(s), (nq[s] - 1) & 1u, a.status);
-          if (!ok || *(volatile int*)&abort_sh) { ok = false; break; }
-          const int h = w.hk * a.G + t / a.tokens, n = (t % a.tokens) * ROWS;
-          mbar_arrive_tx(q_full(s), L::TILE);
-#pragma unroll
-          for (int x = 0; x < L::ATOMS; ++x)
-            tma_load_4d(sQ(s) + x * L::ATOM, &a.q.map, 64 * x, n, a.q.h_on ? h : 0, a.q.b_on ? w.b : 0, q_full(s));
-          ++nq[s];
-        }
         for (int j = 0; ok && j < 2 * w.tiles; ++j) {
-          const int i = nk % L::STAGES;
-          if (nk >= L::STAGES) ok = mbar_wait(empty(i), (nk / L::STAGES - 1) & 1u, a.status);
-          if (!ok || *(volatile int*)&abort_sh) { ok = false; break; }
-          const TensorMap& m = (j & 1) ? a.v : a.k;
-          mbar_arrive_tx(full(i), L::TILE);
-#pragma unroll
-          for (int x = 0; x < L::ATOMS; ++x)
-            tma_load_4d(sKV(i) + x * L::ATOM, &m.map, 64 * x, (w.k0 + (j >> 1)) * KEYS, m.h_on ? w.hk : 0,
-                        m.b_on ? w.b : 0, full(i));
+          if (j < SLOTS && 2 * w.pair + j < row_tiles) {
+            const int t = 2 * w.pair + j;
+            load(sQ(nq), a.q, (t % a.tokens) * ROWS, w.hk * a.G + t / a.tokens, w.b, q_full(nq), q_empty(nq),
+                 nq >= QBUFS, (nq / QBUFS - 1) & 1u);
+            if (!ok) break;
+            ++nq;
+          }
+          load(sKV(nk), (j & 1) ? a.v : a.k, (w.k0 + (j >> 1)) * KEYS, w.hk, w.b, full(nk), empty(nk), nk >= L::STAGES,
+               (nk / L::STAGES - 1) & 1u);
+          if (!ok) break;
           ++nk;
         }
       }
       // every copy has landed before this CTA's shared memory goes
-      for (int s = 0; s < SLOTS; ++s)
-        if (nq[s] > 0) mbar_wait(q_full(s), (nq[s] - 1) & 1u, a.status);
-      for (uint32_t x = nk > L::STAGES ? nk - L::STAGES : 0; x < nk; ++x)
-        mbar_wait(full(x % L::STAGES), (x / L::STAGES) & 1u, a.status);
+      for (uint32_t x = nq > QBUFS ? nq - QBUFS : 0; x < nq; ++x) mbar_wait(q_full(x), (x / QBUFS) & 1u, a.status);
+      for (uint32_t x = nk > L::STAGES ? nk - L::STAGES : 0; x < nk; ++x) mbar_wait(full(x), (x / L::STAGES) & 1u, a.status);
       if (!ok) atomicExch(&abort_sh, 1);
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------ MMAs (warp-uniform, one lane's predicate on)
-    uint32_t nk = 0, nq[SLOTS] = {0, 0}, np[SLOTS] = {0, 0};
+    uint32_t nk = 0, nq = 0, np[SLOTS] = {0, 0}, no[SLOTS] = {0, 0};
     const uint32_t e = elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -345,15 +372,16 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
       fence_after();
       return ok;
     };
-    // S of a slot from K in stage i, n keys (a multiple of 16)
-    auto issue_s = [&](int s, int i, int n) {
-      const uint64_t dq = sdesc(sQ(s), 16, 1024), dk = sdesc(sKV(i), 16, 1024);
+    // S of a slot from K in stage x, n keys (a multiple of 16)
+    auto issue_s = [&](int s, uint32_t q, uint32_t x, int n) {
+      const uint64_t dq = sdesc(sQ(q), 16, 1024), dk = sdesc(sKV(x), 16, 1024);
       const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint64_t o = (uint64_t)(((ks >> 2) * L::ATOM + (ks & 3) * 32) >> 4);
         mma_f16_if(e, tmem + 128u * (uint32_t)s, dq + o, dk + o, idesc, ks > 0 ? 1u : 0u);
       }
+      mma_commit_if(e, s_full(s));
     };
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
       const Item w = item_of(a, it, __shfl_sync(0xffffffffu, kept(a, it), 0));
@@ -361,63 +389,67 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
       const int slots = 2 * w.pair + 1 < row_tiles ? 2 : 1;
       const int last = w.valid - (w.k0 + w.tiles - 1) * KEYS;       // keys of the last tile
       auto n16 = [&](int j) { return j == w.tiles - 1 && last < KEYS ? (last + 15) & ~15 : KEYS; };
-      if (!wait(full(nk % L::STAGES), (nk / L::STAGES) & 1u)) break;
       for (int s = 0; ok && s < slots; ++s) {
-        if (!wait(q_full(s), nq[s] & 1u)) break;
-        ++nq[s];
-        issue_s(s, nk % L::STAGES, n16(0));
-        mma_commit_if(e, s_full(s));
-        if (w.tiles == 1) mma_commit_if(e, q_empty(s));
-        if (s == slots - 1) mma_commit_if(e, empty(nk % L::STAGES));
+        if (!wait(q_full(nq + s), ((nq + s) / QBUFS) & 1u)) break;
+        if (s == 0 && !wait(full(nk), (nk / L::STAGES) & 1u)) break;
+        issue_s(s, nq + s, nk, n16(0));
+        if (w.tiles == 1) mma_commit_if(e, q_empty(nq + s));
+        if (s == slots - 1) mma_commit_if(e, empty(nk));
       }
       ++nk;
       for (int j = 0; ok && j < w.tiles; ++j) {
         // V_j in stage nk, K_{j+1} in the next one
-        const int iv = nk % L::STAGES, ik = (nk + 1) % L::STAGES;
         const bool more = j + 1 < w.tiles;
-        if (!wait(full(iv), (nk / L::STAGES) & 1u)) break;
+        if (!wait(full(nk), (nk / L::STAGES) & 1u)) break;
         const int n = n16(j);
         if (!more && (last & 15) != 0) {
           // rows of V past the last kept key, up to the MMA's K
           for (int x = lane; x < (n - last) * (D / 8); x += 32) {
             const int row = last + x / (D / 8), c = x % (D / 8);
-            const uint32_t at = sKV(iv) + (c >> 3) * L::ATOM + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            const uint32_t at = sKV(nk) + (c >> 3) * L::ATOM + row * 128 + (((c & 7) ^ (row & 7)) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
           }
           fence_proxy_async();
           __syncwarp();
         }
-        if (more && !wait(full(ik), ((nk + 1) / L::STAGES) & 1u)) break;
+        if (more && !wait(full(nk + 1), ((nk + 1) / L::STAGES) & 1u)) break;
         for (int s = 0; ok && s < slots; ++s) {
-          if (!wait(p_full(s), np[s] & 1u)) break;
-          ++np[s];
-          const uint64_t dv = sdesc(sKV(iv), L::ATOM, 1024);
+          // O is this item's once the last one's has been read
+          if (j == 0 && no[s]++ > 0 && !wait(o_empty(s), no[s] & 1u)) break;
+          const uint64_t dv = sdesc(sKV(nk), L::ATOM, 1024);
           const uint32_t pa = tmem + 128u * (uint32_t)s, od = tmem + O_COL + 128u * (uint32_t)s;
+          if (!wait(p_full(s, 0), np[s] & 1u)) break;
           if (n == KEYS) {
 #pragma unroll
-            for (int kk = 0; kk < KEYS / 16; ++kk)
+            for (int kk = 0; kk < 4; ++kk)
               mma_ts_if(e, od, pa + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kk > 0 || j > 0) ? 1u : 0u);
+            if (!wait(p_full(s, 1), np[s] & 1u)) break;
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              mma_ts_if(e, od, pa + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, 1u);
           } else {
+            if (!wait(p_full(s, 1), np[s] & 1u)) break;
             for (int kk = 0; kk < n / 16; ++kk)
               mma_ts_if(e, od, pa + 8u * kk, dv + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kk > 0 || j > 0) ? 1u : 0u);
           }
-          if (s == slots - 1) mma_commit_if(e, empty(iv));
+          ++np[s];
+          if (s == slots - 1) mma_commit_if(e, empty(nk));
           if (!more) {
             mma_commit_if(e, o_full(s));
           } else {
-            issue_s(s, ik, n16(j + 1));
-            mma_commit_if(e, s_full(s));
-            if (j + 2 == w.tiles) mma_commit_if(e, q_empty(s));
-            if (s == slots - 1) mma_commit_if(e, empty(ik));
+            issue_s(s, nq + s, nk + 1, n16(j + 1));
+            if (j + 2 == w.tiles) mma_commit_if(e, q_empty(nq + s));
+            if (s == slots - 1) mma_commit_if(e, empty(nk + 1));
           }
         }
         nk += more ? 2 : 1;
       }
+      nq += slots;
     }
     if (!ok && lane == 0) atomicExch(&abort_sh, 1);
     // one more commit: its arrival means that every MMA has completed
-    mma_commit_if(e, drain);
-    mbar_wait(drain, 0, a.status);
+    mma_commit_if(e, bar(DRAIN));
+    mbar_wait(bar(DRAIN), 0, a.status);
     __syncwarp();
   }
   fence_before();
@@ -427,40 +459,40 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
-// Joins the shares of a row: grid (row tiles, B * Hkv), a warp per row at a time.
+// Joins the shares of a row: grid (row tiles * 16, B * Hkv), a warp per row.
 template <int D, bool H>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
-  const int t = blockIdx.x, bk = blockIdx.y, lane = threadIdx.x & 31;
+  const int t = blockIdx.x / 16, bk = blockIdx.y, lane = threadIdx.x & 31;
   const int b = bk / a.Hkv, hk = bk % a.Hkv;
   const int g = t / a.tokens, h = hk * a.G + g;
   const size_t first = ((size_t)bk * a.pairs + t / 2) * a.splits;    // item of share 0
-  for (int r = threadIdx.x >> 5; r < ROWS; r += 8) {
-    const int n = (t % a.tokens) * ROWS + r;
-    if (n >= a.Nq) break;
-    auto row = [&](int s) { return ((first + s) * SLOTS + (t & 1)) * ROWS + r; };
-    float m = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.stat[row(s)].x);
-    m = warp_maxf(m);
-    float l = 0.f, o[D / 32];
+  const int r = (blockIdx.x % 16) * 8 + (threadIdx.x >> 5), n = (t % a.tokens) * ROWS + r;
+  if (n >= a.Nq) return;
+  auto row = [&](int s) { return ((first + s) * SLOTS + (t & 1)) * ROWS + r; };
+  float m = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.stat[row(s)].x);
+  m = warp_maxf(m);
+  float l = 0.f, o[D / 32];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-    if (m > -INFINITY)
-      for (int s = 0; s < a.splits; ++s) {
-        const float2 st = a.stat[row(s)];
-        const float f = exp2f(st.x - m);
-        l += f * st.y;
-        const float* src = a.part + row(s) * D + lane * (D / 32);
+  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+  if (m > -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+      const float2 st = a.stat[row(s)];
+      const float f = exp2f(st.x - m);
+      l += f * st.y;
+      const float* src = a.part + row(s) * D + lane * (D / 32);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
-      }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    char* dst = a.out.data + 2 * (b * a.out.b + h * a.out.h + (int64_t)n * a.out.n) + lane * (D / 16);
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-      *reinterpret_cast<uint32_t*>(dst + 4 * e) = pack2<H>(o[2 * e] * inv, o[2 * e + 1] * inv);
-    if (lane == 0 && a.lse != nullptr)
-      a.lse[((size_t)b * a.Hq + h) * a.Nq + n] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
+    }
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  char* dst = a.out.data + 2 * (b * a.out.b + h * a.out.h + (int64_t)n * a.out.n) + lane * (D / 16);
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+    *reinterpret_cast<uint32_t*>(dst + 4 * e) = pack2<H>(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[((size_t)b * a.Hq + h) * a.Nq + n] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 static void plan(const Problem& p, Args* a) {
@@ -484,7 +516,7 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kernel<D, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
   if (e != cudaSuccess) return e;
   kernel<D, H><<<std::min(a.items, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
-  if (a.splits > 1) join_kernel<D, H><<<dim3(a.G * a.tokens, a.B * a.Hkv), 256, 0, s>>>(a);
+  if (a.splits > 1) join_kernel<D, H><<<dim3(a.G * a.tokens * (ROWS / 8), a.B * a.Hkv), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
