@@ -3,9 +3,9 @@
 //   D_i = dO_i . O_i,  P = exp(S - lse),  dV = P^T dO,  dS = P (dO V^T - D),
 //   dQ = scale dS K,  dK = scale dS^T Q   (a key head sums over its query heads)
 //
-// Four launches: row_kernel forms D and lse log2 e once; keys_kernel (dK, dV)
-// holds a tile of 128 keys and streams the queries; rows_kernel (dQ) holds a
-// tile of 128 queries and streams the keys; sum_kernel joins the shares of dK
+// Four launches: stat_kernel forms D and lse log2 e of the rows; rows_kernel (dQ)
+// holds a tile of 128 queries and streams the keys; keys_kernel (dK, dV) holds a
+// tile of 128 keys and streams the queries; sum_kernel joins the shares of dK
 // and dV. S and dP are formed twice, seven products of 128x128x128 a tile pair
 // where five would do: adding dQ up over key tiles would take float32 atomics
 // (Nk / 128 times Nq d of them, in an order that changes) or one CTA for
@@ -13,14 +13,10 @@
 //
 // Both kernels: one persistent CTA per SM, eight warps on the elementwise part
 // (each thread one row of the tile's TMEM lanes and half of its 128 columns),
-// one warp on TMA, one on MMAs. P and dS are rounded to bf16 (the operand type
-// of the MMA) and written over their S and dP in TMEM, the lower 64 columns'
-// values at 0..31, the upper ones' at 64..95, so that neither half of the
-// warps writes over what the other half has yet to read; they are the A operand of the
-// second product of each chain. The chains S -> P -> dV and dP -> dS -> dK
-// alternate, so that the tensor cores work on one while the warps work on the other.
-// Products have N = 128 throughout (N = 64 runs at half the rate). Sums, P
-// before rounding and all statistics are float32.
+// one warp on TMA, one on MMAs. P and dS are rounded to bf16, the operand type
+// of the MMA, in TMEM, where they are the A operand of the second product of
+// each chain. Products have N = 128 throughout (N = 64 runs at half the rate).
+// Sums, P before rounding and all statistics are float32.
 //
 // Bounded waits as in the forward kernels.
 #include "cross_tc.cuh"
@@ -31,11 +27,12 @@ namespace bwd {
 
 using namespace tc;
 
-constexpr int TILE = 128, EW_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9, THREADS = 320;
+constexpr int TILE = 128, EW_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9, OUT_WARP0 = 12;
+constexpr int KEYS_THREADS = 320, ROWS_THREADS = 512;
 constexpr int STAGES = 5;
 
 struct Args {
-  TensorMap q, k, v, dout;
+  TensorMap q, k, v, dout, dqm;              // dqm: dq
   View o, dov, dq, dk, dv;                   // o: out; dov: dout
   const float* lse;
   const int32_t* key_len;                    // kept keys per item (after packing), or null
@@ -45,6 +42,8 @@ struct Args {
   int qtiles, ktiles;
   int ksplits, kper, kitems;                 // shares of a key tile's query tiles, tiles per share
   int qsplits, qitems;                       // shares of a query tile's key tiles
+  int q_per;                                 // items of a CTA in a row; 0: every gridDim.x-th
+  int stay;                                  // at most two key tiles: K stays in shared memory
   float scale, sl2;
   float *lse2, *delta;                       // [B * Hq][NqP]
   float* part;                               // [kitems][2][128][d] shares of dK and dV
@@ -52,32 +51,43 @@ struct Args {
 };
 
 // ------------------------------------------------------------------ D and lse
-// One 16-lane (d = 128) or 8-lane (d = 64) group per row: 16 bytes of O and of
-// dO per lane, a shuffle sum. Rows past Nq get lse = +inf (P = 0) and D = 0.
+// 16 lanes (d = 128; 8 for 64) a row, four rows a lane in flight. Rows past Nq get
+// lse = +inf (so P = 0) and D = 0. Bound by HBM: O and dO are read once.
+// grid (NqP / (1024 / LPR), B * Hq). Forming D inside rows_kernel instead (four
+// warps beside its elementwise ones) was slower: their instructions are the
+// scarce thing there.
 template <int D>
-__global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ Args a) {
-  constexpr int LPR = D / 8;
-  const int n = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, l = threadIdx.x % LPR;
-  const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
-  if (a.key_len != nullptr && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
-    item_len(a.key_len, a.Nk, b, a.status, true);
-  float s = 0.f;
-  if (n < a.Nq) {
-    const uint4 x = *reinterpret_cast<const uint4*>(a.o.data + 2 * (b * a.o.b + h * a.o.h + (int64_t)n * a.o.n + 8 * l));
-    const uint4 y = *reinterpret_cast<const uint4*>(a.dov.data + 2 * (b * a.dov.b + h * a.dov.h + (int64_t)n * a.dov.n + 8 * l));
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+__global__ void __launch_bounds__(256) stat_kernel(const __grid_constant__ Args a) {
+  constexpr int LPR = D / 8, ROWS = 256 / LPR;
+  const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq, l = threadIdx.x % LPR;
+  const int n0 = blockIdx.x * (4 * ROWS) + threadIdx.x / LPR;
+  if (a.key_len != nullptr && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) item_len(a.key_len, a.Nk, b, a.status, true);
+  const char* po = a.o.data + 2 * (b * a.o.b + h * a.o.h + 8 * l);
+  const char* pd = a.dov.data + 2 * (b * a.dov.b + h * a.dov.h + 8 * l);
+  uint4 x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s = fmaf(bf_lo(xs[i]), bf_lo(ys[i]), s);
-      s = fmaf(bf_hi(xs[i]), bf_hi(ys[i]), s);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = min(n0 + i * ROWS, a.Nq - 1);
+    x[i] = __ldcs(reinterpret_cast<const uint4*>(po + 2 * n * a.o.n));
+    y[i] = *reinterpret_cast<const uint4*>(pd + 2 * n * a.dov.n);
   }
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (l == 0 && n < a.NqP) {
-    const size_t at = (size_t)bh * a.NqP + n;
-    a.delta[at] = n < a.Nq ? s : 0.f;
-    a.lse2[at] = n < a.Nq ? a.lse[(size_t)bh * a.Nq + n] * 1.4426950408889634f : INFINITY;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      s = fmaf(bf_lo(xs[c]), bf_lo(ys[c]), s);
+      s = fmaf(bf_hi(xs[c]), bf_hi(ys[c]), s);
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int n = n0 + i * ROWS;
+    if (l == 0 && n < a.NqP) {
+      const size_t at = (size_t)bh * a.NqP + n;
+      a.delta[at] = n < a.Nq ? s : 0.f;
+      a.lse2[at] = n < a.Nq ? a.lse[(size_t)bh * a.Nq + n] * 1.4426950408889634f : INFINITY;
+    }
   }
 }
 
@@ -86,7 +96,7 @@ struct Lay {
   static constexpr int ATOMS = D / 64;
   static constexpr int ATOM = TILE * 128;
   static constexpr int BYTES = ATOM * ATOMS;           // a tile of 128 rows
-  static constexpr int OFF_ROW = (2 + STAGES) * BYTES; // two slots of lse and D of 128 queries
+  static constexpr int OFF_ROW = (2 + STAGES) * BYTES; // two sets of lse and D of 128 queries
   static constexpr int OFF_BAR = OFF_ROW + 2048;
   static constexpr int SMEM = OFF_BAR + 512;
   static_assert(SMEM <= 232448, "shared memory of a block");
@@ -105,17 +115,18 @@ __device__ __forceinline__ void product_nt(uint32_t e, uint32_t d, uint32_t sa, 
   }
 }
 // D (TMEM, 128 x d) (+)= A (TMEM, bf16, 16 rows of B a step) B, B a tile of rows in shared memory.
-template <int D>
+// GAP: A's values of B's rows 64.. are GAP columns further on.
+template <int D, int GAP>
 __device__ __forceinline__ void product_ts(uint32_t e, uint32_t d, uint32_t ta, uint32_t sb, int steps, bool add) {
   const uint64_t db = sdesc(sb, Lay<D>::ATOM, 1024);
   const uint32_t idesc = IDESC | (1u << 16) | ((uint32_t)(D >> 3) << 17);
   if (steps == TILE / 16) {
 #pragma unroll
     for (int kk = 0; kk < TILE / 16; ++kk)
-      mma_ts_if(e, d, ta + 8u * kk + (kk >= 4 ? 32u : 0u), db + (uint64_t)((kk * 2048) >> 4), idesc, (kk > 0 || add) ? 1u : 0u);
+      mma_ts_if(e, d, ta + 8u * kk + (kk >= 4 ? (uint32_t)GAP : 0u), db + (uint64_t)((kk * 2048) >> 4), idesc, (kk > 0 || add) ? 1u : 0u);
   } else {
     for (int kk = 0; kk < steps; ++kk)
-      mma_ts_if(e, d, ta + 8u * kk + (kk >= 4 ? 32u : 0u), db + (uint64_t)((kk * 2048) >> 4), idesc, (kk > 0 || add) ? 1u : 0u);
+      mma_ts_if(e, d, ta + 8u * kk + (kk >= 4 ? (uint32_t)GAP : 0u), db + (uint64_t)((kk * 2048) >> 4), idesc, (kk > 0 || add) ? 1u : 0u);
   }
 }
 template <int D>
@@ -125,7 +136,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const TensorMap& m, int 
   for (int x = 0; x < Lay<D>::ATOMS; ++x)
     tma_load_4d(dst + x * Lay<D>::ATOM, &m.map, 64 * x, n, m.h_on ? h : 0, m.b_on ? b : 0, bar);
 }
-__device__ __forceinline__ void ew_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Shared start and end of both kernels.
 struct Block {
@@ -169,18 +179,23 @@ __device__ __forceinline__ void finish(const Block& k) {
 }
 
 // ------------------------------------------------------------------ dK, dV
-// TMEM: S^T 0, dP^T 128, dV 256, dK 384. Lanes are keys, columns queries.
+// TMEM: S^T 0, dP^T 128, dV 256, dK 384. Lanes are keys, columns queries. P and
+// dS stand over their S and dP, the lower 64 columns' values at 0..31, the upper
+// ones' at 64..95, so that neither half of the warps writes over what the other
+// has yet to read. The chains S -> P -> dV and dP -> dS -> dK alternate: the
+// tensor cores work on one while the warps work on the other.
 // What stands in the rows of k and v past the kept ones only reaches their
 // own lanes, which are not written.
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1) keys_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_constant__ Args a) {
   using L = Lay<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
-  enum { FIXED_FULL, FIXED_EMPTY, S_FULL, P_FULL, DP_FULL, DS_FULL, ACC_FULL, ACC_EMPTY, FULL, EMPTY = FULL + STAGES,
-         DRAIN = EMPTY + STAGES, NBAR };
+  enum { FIXED_FULL, FIXED_EMPTY, S_FULL, P_FULL, DP_FULL, DS_FULL, ACC_FULL, ACC_EMPTY, ROW_FULL, ROW_READ = ROW_FULL + 2,
+         FULL = ROW_READ + 2, EMPTY = FULL + STAGES, DRAIN = EMPTY + STAGES, NBAR };
   unsigned counts[NBAR];
 #pragma unroll
-  for (int i = 0; i < NBAR; ++i) counts[i] = (i == P_FULL || i == DS_FULL || i == ACC_EMPTY) ? EW_WARPS : 1;
+  for (int i = 0; i < NBAR; ++i)
+    counts[i] = (i == P_FULL || i == DS_FULL || i == ACC_EMPTY || i == ROW_READ || i == ROW_READ + 1) ? EW_WARPS : 1;
   Block k;
   if (!start<D>(smem, NBAR, counts, a.status, k)) return;
   auto bar = [&](int i) { return k.bar0 + 8u * (uint32_t)i; };
@@ -198,106 +213,88 @@ __global__ void __launch_bounds__(THREADS, 1) keys_kernel(const __grid_constant_
   auto kept = [&](int it) { return item_len(a.key_len, a.Nk, it / (a.ksplits * a.ktiles * a.Hkv), nullptr, false); };
 
   if (k.warp < EW_WARPS) {
-    const int half = k.warp >> 2, tid = threadIdx.x;
+    const int half = k.warp >> 2;
     const uint32_t tb = k.tmem + ((uint32_t)((k.warp & 3) * 32) << 16);
     const uint32_t sc = tb + 64u * (uint32_t)half, dc = tb + 128u + 64u * (uint32_t)half;
-    float* rowsm = reinterpret_cast<float*>(smem + L::OFF_ROW);       // [2][lse 128, D 128]
     uint32_t nt = 0, ni = 0;                 // tiles, items seen
     bool ok = true;
+    auto wait = [&](int i, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, a.status));
+      fence_after();
+      return ok;
+    };
+    auto arrive = [&](int i) {
+      fence_before();
+      __syncwarp();
+      if (k.lane == 0) mbar_arrive(bar(i));
+    };
     for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
       int b, hk, kt, t0;
       const int tiles = item(it, kept(it), b, hk, kt, t0);
       if (tiles == 0) continue;
-      // this thread's value (lse of column tid, or D of column tid - 128) of a tile
-      auto row_value = [&](int t) {
-        const int h = hk * a.G + t / a.qtiles;
-        const float* src = tid < 128 ? a.lse2 : a.delta;
-        return src[((size_t)b * a.Hq + h) * a.NqP + (t % a.qtiles) * TILE + (tid & 127)];
-      };
-      rowsm[(nt & 1) * 256 + tid] = row_value(t0);
-      ew_sync();
       for (int j = 0; j < tiles; ++j, ++nt) {
-        const float next = j + 1 < tiles ? row_value(t0 + j + 1) : 0.f;
-        const float4* lse4 = reinterpret_cast<const float4*>(rowsm + (nt & 1) * 256 + 64 * half);
+        // lse log2 e and D of the tile's queries: one value per column, read by all lanes at once
+        const float4* lse4 = reinterpret_cast<const float4*>(smem + L::OFF_ROW + 1024 * (nt & 1)) + 16 * half;
         const float4* del4 = lse4 + 32;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(S_FULL), nt & 1u, a.status));
+        if (!wait(ROW_FULL + (nt & 1), (nt >> 1) & 1u) || !wait(S_FULL, nt & 1u)) break;
+        uint32_t x[64], w[32];
         float p[64];
-        if (ok) {
-          fence_after();
-          uint32_t x[64], pw[32];
-          tmem_ld32p(sc, x);
-          tmem_ld32p(sc + 32u, x + 32);
-          tmem_ld_wait();
+        tmem_ld32p(sc, x);
+        tmem_ld32p(sc + 32u, x + 32);
+        tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float4 s = lse4[c];
-            p[4 * c] = ex2(fmaf(__uint_as_float(x[4 * c]), a.sl2, -s.x));
-            p[4 * c + 1] = ex2(fmaf(__uint_as_float(x[4 * c + 1]), a.sl2, -s.y));
-            p[4 * c + 2] = ex2(fmaf(__uint_as_float(x[4 * c + 2]), a.sl2, -s.z));
-            p[4 * c + 3] = ex2(fmaf(__uint_as_float(x[4 * c + 3]), a.sl2, -s.w));
-            pw[2 * c] = pack2<false>(p[4 * c], p[4 * c + 1]);
-            pw[2 * c + 1] = pack2<false>(p[4 * c + 2], p[4 * c + 3]);
-          }
-          tmem_st32p(sc, pw);
-          tmem_st_wait();
-          fence_before();
-          __syncwarp();
-          if (k.lane == 0) mbar_arrive(bar(P_FULL));
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(DP_FULL), nt & 1u, a.status));
+        for (int c = 0; c < 16; ++c) {
+          const float4 s = lse4[c];
+          const uint64_t sl = f2(a.sl2, a.sl2);
+          float u0, u1, u2, u3;
+          unf2(ffma2(f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sl, f2(-s.x, -s.y)), u0, u1);
+          unf2(ffma2(f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sl, f2(-s.z, -s.w)), u2, u3);
+          p[4 * c] = ex2(u0);
+          p[4 * c + 1] = ex2(u1);
+          p[4 * c + 2] = ex2(u2);
+          p[4 * c + 3] = ex2(u3);
+          w[2 * c] = pack2<false>(p[4 * c], p[4 * c + 1]);
+          w[2 * c + 1] = pack2<false>(p[4 * c + 2], p[4 * c + 3]);
         }
-        if (ok) {
-          fence_after();
-          uint32_t x[64], w[32];
-          tmem_ld32p(dc, x);
-          tmem_ld32p(dc + 32u, x + 32);
-          tmem_ld_wait();
+        tmem_st32p(sc, w);
+        tmem_st_wait();
+        arrive(P_FULL);
+        if (!wait(DP_FULL, nt & 1u)) break;
+        tmem_ld32p(dc, x);
+        tmem_ld32p(dc + 32u, x + 32);
+        tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float4 s = del4[c];
-            const float d0 = p[4 * c] * (__uint_as_float(x[4 * c]) - s.x);
-            const float d1 = p[4 * c + 1] * (__uint_as_float(x[4 * c + 1]) - s.y);
-            const float d2 = p[4 * c + 2] * (__uint_as_float(x[4 * c + 2]) - s.z);
-            const float d3 = p[4 * c + 3] * (__uint_as_float(x[4 * c + 3]) - s.w);
-            w[2 * c] = pack2<false>(d0, d1);
-            w[2 * c + 1] = pack2<false>(d2, d3);
-          }
-          tmem_st32p(dc, w);
-          tmem_st_wait();
-          fence_before();
-          __syncwarp();
-          if (k.lane == 0) mbar_arrive(bar(DS_FULL));
+        for (int c = 0; c < 16; ++c) {
+          const float4 s = del4[c];
+          const float d0 = p[4 * c] * (__uint_as_float(x[4 * c]) - s.x);
+          const float d1 = p[4 * c + 1] * (__uint_as_float(x[4 * c + 1]) - s.y);
+          const float d2 = p[4 * c + 2] * (__uint_as_float(x[4 * c + 2]) - s.z);
+          const float d3 = p[4 * c + 3] * (__uint_as_float(x[4 * c + 3]) - s.w);
+          w[2 * c] = pack2<false>(d0, d1);
+          w[2 * c + 1] = pack2<false>(d2, d3);
         }
-        if (j + 1 < tiles) rowsm[((nt + 1) & 1) * 256 + tid] = next;
-        ew_sync();
+        tmem_st32p(dc, w);
+        tmem_st_wait();
+        arrive(DS_FULL);
+        if (k.lane == 0) mbar_arrive(bar(ROW_READ + (nt & 1)));
       }
       // shares of dV (the first four warps) and dK
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(ACC_FULL), ni & 1u, a.status));
-      ++ni;
-      if (ok) {
-        fence_after();
-        float* dst = a.part + (((size_t)it * 2 + half) * TILE + (k.warp & 3) * 32 + k.lane) * D;
+      if (!ok || !wait(ACC_FULL, ni++ & 1u)) break;
+      float* dst = a.part + (((size_t)it * 2 + half) * TILE + (k.warp & 3) * 32 + k.lane) * D;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld32p(tb + 256u + 128u * (uint32_t)half + 32u * c, x);
-          tmem_ld_wait();
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        tmem_ld32p(tb + 256u + 128u * (uint32_t)half + 32u * c, x);
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) store32(dst + 32 * c + e, x + e);
-        }
-        fence_before();
-        __syncwarp();
-        if (k.lane == 0) mbar_arrive(bar(ACC_EMPTY));
-      } else {
-        k.abort_flag[1] = 1;
+        for (int e = 0; e < 32; e += 8) store32(dst + 32 * c + e, x + e);
       }
-      // the eight warps leave together: they meet at barriers in every item
-      ew_sync();
-      ok = k.abort_flag[1] == 0;
+      arrive(ACC_EMPTY);
     }
     if (!ok) *k.abort_flag = 1;
   } else if (k.warp == TMA_WARP) {
     if (k.lane == 0) {
-      uint32_t nf = 0, nk = 0;
+      uint32_t nf = 0, nk = 0, nr = 0;
       bool ok = true;
       for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
         int b, hk, kt, t0;
@@ -316,11 +313,22 @@ __global__ void __launch_bounds__(THREADS, 1) keys_kernel(const __grid_constant_
           // Q_0, dO_0, Q_1, dO_1, ...
           if (nk >= STAGES) ok = mbar_wait(bar(EMPTY + nk % STAGES), (nk / STAGES - 1) & 1u, a.status);
           if (!ok || *k.abort_flag) { ok = false; break; }
-          const int t = t0 + (j >> 1);
-          load_tile<D>(stage(nk), (j & 1) ? a.dout : a.q, (t % a.qtiles) * TILE, hk * a.G + t / a.qtiles, b, bar(FULL + nk % STAGES));
+          const int t = t0 + (j >> 1), h = hk * a.G + t / a.qtiles, n = (t % a.qtiles) * TILE;
+          load_tile<D>(stage(nk), (j & 1) ? a.dout : a.q, n, h, b, bar(FULL + nk % STAGES));
+          if ((j & 1) == 0) {                // and the tile's lse and D
+            const uint32_t i = nr & 1u, to = k.base + L::OFF_ROW + 1024u * i;
+            if (nr >= 2) ok = mbar_wait(bar(ROW_READ + i), (nr / 2 - 1) & 1u, a.status);
+            if (!ok) { ++nk; break; }
+            const size_t at = ((size_t)b * a.Hq + h) * a.NqP + n;
+            mbar_arrive_tx(bar(ROW_FULL + i), 1024);
+            bulk_load(to, a.lse2 + at, 512, bar(ROW_FULL + i));
+            bulk_load(to + 512, a.delta + at, 512, bar(ROW_FULL + i));
+            ++nr;
+          }
         }
       }
       if (nf > 0) mbar_wait(bar(FIXED_FULL), (nf - 1) & 1u, a.status);
+      for (uint32_t x = nr > 2 ? nr - 2 : 0; x < nr; ++x) mbar_wait(bar(ROW_FULL + (x & 1u)), (x >> 1) & 1u, a.status);
       for (uint32_t x = nk > STAGES ? nk - STAGES : 0; x < nk; ++x) mbar_wait(bar(FULL + x % STAGES), (x / STAGES) & 1u, a.status);
       if (!ok) *k.abort_flag = 1;
     }
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 1) keys_kernel(const __grid_constant_
         if (!wait(P_FULL, nt & 1u)) break;
         // the accumulators are this item's once the last item's have been read
         if (j == 0 && ni > 0 && !wait(ACC_EMPTY, (ni - 1) & 1u)) break;
-        product_ts<D>(e, k.tmem + 256u, k.tmem, stage(nk + 1), TILE / 16, j > 0);           // dV += P^T dO
+        product_ts<D, 32>(e, k.tmem + 256u, k.tmem, stage(nk + 1), TILE / 16, j > 0);           // dV += P^T dO
         mma_commit_if(e, bar(EMPTY + (nk + 1) % STAGES));
         if (more) {
           if (!wait_stage(nk + 2)) break;
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1) keys_kernel(const __grid_constant_
           mma_commit_if(e, bar(S_FULL));
         }
         if (!wait(DS_FULL, nt & 1u)) break;
-        product_ts<D>(e, k.tmem + 384u, k.tmem + 128u, stage(nk), TILE / 16, j > 0);        // dK += dS^T Q
+        product_ts<D, 32>(e, k.tmem + 384u, k.tmem + 128u, stage(nk), TILE / 16, j > 0);        // dK += dS^T Q
         mma_commit_if(e, bar(EMPTY + nk % STAGES));
         if (more) {
           if (!wait_stage(nk + 3)) break;
@@ -380,20 +388,47 @@ __global__ void __launch_bounds__(THREADS, 1) keys_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ dQ
-// TMEM: S 0 and 256 (two tiles), dP 128, dQ 384. Lanes are queries, columns keys.
-template <int D>
-__global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant__ Args a) {
+// TMEM: S 0, dP 128, dS 256 and 320 (two tiles), dQ 384. Lanes are queries,
+// columns keys. The warps take S and dP into registers and say so at once, and
+// dS has columns of its own, so the tensor cores form the next tile's S and
+// dP while the warps work on this one's; dQ of tile t is issued after S and dP
+// of tile t + 1, across items too.
+// Shared memory, seven tiles: one of dO, one of V, and
+//  - more than two key tiles: two that hold an item's Q and then its dQ on the
+//    way out (a TMA store: rows straight from registers, 256 bytes a lane, took
+//    5,000 clocks a tile); three of K, in use from S to dQ (with two the next but
+//    one's copy, which waits for dQ, was 1,300 clocks late);
+//  - one or two key tiles (STAY): three of Q and dQ, because two made the next but
+//    one's Q wait for the store, 2,000 clocks an item; two of K, copied when
+//    the key head changes. A CTA's items then follow one another in a head.
+// One TMA warp brings Q and dO (the next dO, which has to wait for its buffer, is
+// asked into L2 meanwhile), one K and V. Four warps write dQ out.
+template <int D, bool STAY>
+__global__ void __launch_bounds__(ROWS_THREADS, 1) rows_kernel(const __grid_constant__ Args a) {
   using L = Lay<D>;
+  static_assert(256 * 176 + 256 * 72 <= ROWS_THREADS * 128, "registers the block owns");
+  constexpr int ROW_TMA_WARP = 10;
   extern __shared__ __align__(1024) unsigned char smem[];
-  enum { FIXED_FULL, FIXED_EMPTY, S_FULL0, S_FULL1, DP_FULL, DS_FULL, ACC_FULL, ACC_EMPTY, FULL, EMPTY = FULL + STAGES,
-         DRAIN = EMPTY + STAGES, NBAR };
+  enum { Q_FULL = 0, Q_READ = 3, DS_FULL = 6, DO_FULL = 8, DO_READ, V_FULL, V_READ, S_FULL, S_READ, DP_FULL, DP_READ,
+         ACC_FULL, ACC_READ, K_FULL, K_READ = K_FULL + 3, DRAIN = K_READ + 3, NBAR };
   unsigned counts[NBAR];
 #pragma unroll
-  for (int i = 0; i < NBAR; ++i) counts[i] = (i == DS_FULL || i == ACC_EMPTY) ? EW_WARPS : 1;
+  for (int i = 0; i < NBAR; ++i)
+    counts[i] = (i == S_READ || i == DP_READ || (i & ~1) == DS_FULL) ? EW_WARPS
+                : i == ACC_READ ? 4
+                : i >= Q_READ && i < Q_READ + 3 ? 2 : 1;       // Q: the MMAs and the store of dQ
   Block k;
   if (!start<D>(smem, NBAR, counts, a.status, k)) return;
   auto bar = [&](int i) { return k.bar0 + 8u * (uint32_t)i; };
-  auto stage = [&](uint32_t i) { return k.base + (2u + i % STAGES) * L::BYTES; };
+  constexpr uint32_t NX = STAY ? 3 : 2, NK = STAY ? 2 : 3;
+  auto sX = [&](uint32_t i) { return k.base + i % NX * L::BYTES; };
+  const uint32_t sdO = k.base + NX * L::BYTES, sV = sdO + L::BYTES;
+  // K of tile t of all, tile j of its item
+  auto k_at = [&](uint32_t t, int j) { return STAY ? (uint32_t)j : t % NK; };
+  auto sK = [&](uint32_t i) { return sV + (1u + i) * L::BYTES; };
+  // this CTA's items: every gridDim.x-th, or q_per in a row
+  const int it0 = a.q_per ? blockIdx.x * a.q_per : blockIdx.x, step = a.q_per ? 1 : gridDim.x;
+  const int end = a.q_per ? min(it0 + a.q_per, a.qitems) : a.qitems;
   // item: query tile qt of (b, h), key tiles [k0, k0 + tiles)
   auto item = [&](int it, int valid, int& b, int& h, int& qt, int& k0) -> int {
     const int split = it % a.qsplits, u = it / a.qsplits;
@@ -405,41 +440,61 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
     return max(0, min(per, all - k0));
   };
   auto kept = [&](int it) { return item_len(a.key_len, a.Nk, it / (a.qsplits * a.qtiles * a.Hq), nullptr, false); };
+  // phase x of a barrier (of a pair of them: use x of the pair) as a whole warp
+  bool ok = true;
+  auto wait = [&](int i, uint32_t x) {
+    ok = __all_sync(0xffffffffu, mbar_wait(bar(i), x & 1u, a.status));
+    fence_after();
+    return ok;
+  };
+  auto wait2 = [&](int i, uint32_t x) { return wait(i + (int)(x & 1u), x >> 1); };
 
+  if (k.warp < EW_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (k.warp < EW_WARPS) {
     const int half = k.warp >> 2, r = (k.warp & 3) * 32 + k.lane;
     const uint32_t tb = k.tmem + ((uint32_t)((k.warp & 3) * 32) << 16);
-    const uint32_t dc = tb + 128u + 64u * (uint32_t)half;
-    uint32_t nt = 0, ni = 0;
-    bool ok = true;
-    for (int it = blockIdx.x; ok && it < a.qitems; it += gridDim.x) {
+    const uint32_t sc = tb + 64u * (uint32_t)half, dc = sc + 128u;
+    auto arrive = [&](int i) {
+      fence_before();
+      __syncwarp();
+      if (k.lane == 0) mbar_arrive(bar(i));
+    };
+    uint32_t nt = 0;
+    // lse log2 e and D of this thread's row, read an item ahead
+    auto row = [&](int it) {
+      if (it >= end) return make_float2(0.f, 0.f);
+      const int u = it / a.qsplits;
+      const size_t at = (size_t)u * TILE + r;            // item order is row order
+      return make_float2(a.lse2[at], a.delta[at]);
+    };
+    float2 next = row(it0);
+    for (int it = it0; ok && it < end; it += step) {
       int b, h, qt, k0;
       const int valid = kept(it);
       const int tiles = item(it, valid, b, h, qt, k0);
-      const size_t at = ((size_t)b * a.Hq + h) * a.NqP + qt * TILE + r;
-      const float lse = a.lse2[at], delta = a.delta[at];
-      for (int j = 0; ok && j < tiles; ++j, ++nt) {
-        const uint32_t sc = tb + 256u * (nt & 1u) + 64u * (uint32_t)half;
+      const float lse = next.x, delta = next.y;
+      next = row(it + step);
+      for (int j = 0; j < tiles; ++j, ++nt) {
         const int left = valid - (k0 + j) * TILE - 64 * half;        // kept keys among this half's columns
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(S_FULL0 + (nt & 1)), (nt >> 1) & 1u, a.status));
-        if (!ok) break;
-        fence_after();
+        if (!wait(S_FULL, nt)) break;
+        uint32_t x[64];
+        tmem_ld32p(sc, x);
+        tmem_ld32p(sc + 32u, x + 32);
+        tmem_ld_wait();
+        arrive(S_READ);
         float p[64];
-        {
-          uint32_t x[64];
-          tmem_ld32p(sc, x);
-          tmem_ld32p(sc + 32u, x + 32);
-          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(__uint_as_float(x[c]), a.sl2, -lse));
+        for (int c = 0; c < 64; c += 2) {
+          unf2(ffma2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2(a.sl2, a.sl2), f2(-lse, -lse)), p[c], p[c + 1]);
+          p[c] = ex2(p[c]);
+          p[c + 1] = ex2(p[c + 1]);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(DP_FULL), nt & 1u, a.status));
-        if (!ok) break;
-        fence_after();
-        uint32_t x[64], w[32];
+        if (!wait(DP_FULL, nt)) break;
         tmem_ld32p(dc, x);
         tmem_ld32p(dc + 32u, x + 32);
         tmem_ld_wait();
+        arrive(DP_READ);
 #pragma unroll
         for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(x[c]) - delta;
         if (left < 64) {
@@ -447,152 +502,212 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
           for (int c = 0; c < 64; ++c)
             if (c >= left) p[c] = 0.f;
         }
+        // dQ of tile nt - 2, the last reader of these columns, came before this dP
+        uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) w[c] = pack2<false>(p[2 * c], p[2 * c + 1]);
-        tmem_st32p(dc, w);
+        tmem_st32p(tb + 256u + 64u * (nt & 1u) + 32u * (uint32_t)half, w);
         tmem_st_wait();
-        fence_before();
-        __syncwarp();
-        if (k.lane == 0) mbar_arrive(bar(DS_FULL));
+        arrive(DS_FULL + (nt & 1));
       }
+    }
+  } else if (k.warp >= OUT_WARP0) {
+    const int tid = threadIdx.x - 32 * OUT_WARP0;                    // this thread's row
+    const uint32_t tb = k.tmem + ((uint32_t)((k.warp - OUT_WARP0) * 32) << 16);
+    uint32_t ni = 0;
+    for (int it = it0; it < end; it += step) {
+      int b, h, qt, k0;
+      const int tiles = item(it, kept(it), b, h, qt, k0);
+      const int n = qt * TILE + tid;
+      if (tiles == 0) {                                  // no keys, or an empty share of them
+        if (a.qsplits > 1) {
+          for (int c = 0; c < D; c += 4)
+            *reinterpret_cast<float4*>(a.qpart + ((size_t)it * TILE + tid) * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (n < a.Nq) {
+          for (int c = 0; c < D; c += 8)
+            *reinterpret_cast<uint4*>(a.dq.data + 2 * (b * a.dq.b + h * a.dq.h + (int64_t)n * a.dq.n + c)) = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      if (ok) wait(ACC_FULL, ni);
+      // the four warps go on together: they meet at a barrier
+      if (!ok) k.abort_flag[1] = 1;
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      ok = k.abort_flag[1] == 0;
       if (!ok) break;
-      if (tiles > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(ACC_FULL), ni & 1u, a.status));
-        if (!ok) break;
-        ++ni;
-        fence_after();
-      }
-      // this thread's half of the row's dQ
-      const int n = qt * TILE + r;
-      char* dst = a.dq.data + 2 * (b * a.dq.b + h * a.dq.h + (int64_t)n * a.dq.n + (D / 2) * half);
-      float* share = a.qpart + ((size_t)it * TILE + r) * D + (D / 2) * half;
+      const uint32_t to = sX(ni);                        // Q's tile: its last product is done
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
-        if (tiles > 0) {
-          tmem_ld32p(tb + 384u + (uint32_t)(D / 2) * half + 32u * c, x);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0u;
+        tmem_ld32p(tb + 384u + 32u * c, x);
+        tmem_ld_wait();
+        if (c == D / 32 - 1) {                           // dQ has been read
+          fence_before();
+          __syncwarp();
+          if (k.lane == 0) mbar_arrive(bar(ACC_READ));
         }
         if (a.qsplits > 1) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) store32(share + 32 * c + e, x + e);
-        } else if (n < a.Nq) {
+          for (int e = 0; e < 32; e += 8) store32(a.qpart + ((size_t)it * TILE + tid) * D + 32 * c + e, x + e);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
+          for (int e = 0; e < 4; ++e) {
             uint32_t w[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              w[y] = pack2<false>(__uint_as_float(x[e + 2 * y]) * a.scale, __uint_as_float(x[e + 2 * y + 1]) * a.scale);
-            *reinterpret_cast<uint4*>(dst + 64 * c + 2 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+              w[y] = pack2<false>(__uint_as_float(x[8 * e + 2 * y]) * a.scale, __uint_as_float(x[8 * e + 2 * y + 1]) * a.scale);
+            const int ch = 4 * c + e;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                         ::"r"(to + (ch >> 3) * L::ATOM + tid * 128 + (((ch & 7) ^ (tid & 7)) << 4)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
           }
         }
       }
-      if (tiles > 0) {
-        fence_before();
-        __syncwarp();
-        if (k.lane == 0) mbar_arrive(bar(ACC_EMPTY));
+      fence_proxy_async();
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      if (tid == 0) {
+        if (a.qsplits == 1) {
+#pragma unroll
+          for (int x = 0; x < L::ATOMS; ++x)
+            tma_store_4d(to + x * L::ATOM, &a.dqm.map, 64 * x, qt * TILE, a.dqm.h_on ? h : 0, a.dqm.b_on ? b : 0);
+          tma_store_commit();
+          tma_store_wait_read();
+        }
+        mbar_arrive(bar(Q_READ + ni % NX));
       }
+      ++ni;
     }
-    if (!ok) *k.abort_flag = 1;
-  } else if (k.warp == TMA_WARP) {
+  } else if (k.warp == TMA_WARP || k.warp == ROW_TMA_WARP) {
     if (k.lane == 0) {
-      uint32_t nf = 0, nk = 0;
-      bool ok = true;
-      for (int it = blockIdx.x; ok && it < a.qitems; it += gridDim.x) {
+      // the copy into a buffer, its use u, once use u - 1 has been read
+      auto load = [&](int full, int read, uint32_t u, uint32_t dst, const TensorMap& m, int n, int h, int b) {
+        if (u > 0) ok = mbar_wait(bar(read), (u - 1) & 1u, a.status);
+        if (*k.abort_flag) ok = false;
+        if (ok) load_tile<D>(dst, m, n, h, b, bar(full));
+        return ok;
+      };
+      uint32_t x = 0, y = 0;                             // copies issued: Q and dO of items, or K and V of key tiles
+      uint32_t k_uses[3] = {0, 0, 0};                    // uses of each K tile
+      int last_head = -1;
+      auto ahead = [&](int it) {
+        if (it >= end) return;
+        int b, h, qt, k0;
+        if (item(it, kept(it), b, h, qt, k0) == 0) return;
+#pragma unroll
+        for (int c = 0; c < L::ATOMS; ++c)
+          tma_prefetch_4d(&a.dout.map, 64 * c, qt * TILE, a.dout.h_on ? h : 0, a.dout.b_on ? b : 0);
+      };
+      for (int it = it0; ok && it < end; it += step) {
         int b, h, qt, k0;
         const int tiles = item(it, kept(it), b, h, qt, k0);
         if (tiles == 0) continue;
-        if (nf > 0) ok = mbar_wait(bar(FIXED_EMPTY), (nf - 1) & 1u, a.status);
-        if (!ok || *k.abort_flag) { ok = false; break; }
-        mbar_arrive_tx(bar(FIXED_FULL), 2 * L::BYTES);
-#pragma unroll
-        for (int x = 0; x < L::ATOMS; ++x) {
-          tma_load_4d(k.base + x * L::ATOM, &a.q.map, 64 * x, qt * TILE, a.q.h_on ? h : 0, a.q.b_on ? b : 0, bar(FIXED_FULL));
-          tma_load_4d(k.base + L::BYTES + x * L::ATOM, &a.dout.map, 64 * x, qt * TILE, a.dout.h_on ? h : 0, a.dout.b_on ? b : 0, bar(FIXED_FULL));
-        }
-        ++nf;
-        for (int j = 0; ok && j < 2 * tiles; ++j, ++nk) {
-          // K_0, V_0, K_1, V_1, ...
-          if (nk >= STAGES) ok = mbar_wait(bar(EMPTY + nk % STAGES), (nk / STAGES - 1) & 1u, a.status);
-          if (!ok || *k.abort_flag) { ok = false; break; }
-          load_tile<D>(stage(nk), (j & 1) ? a.v : a.k, (k0 + (j >> 1)) * TILE, h / a.G, b, bar(FULL + nk % STAGES));
+        if (k.warp == ROW_TMA_WARP) {
+          ahead(it + step);
+          if (!load(Q_FULL + x % NX, Q_READ + x % NX, x / NX, sX(x), a.q, qt * TILE, h, b)) break;
+          ++x;
+          if (!load(DO_FULL, DO_READ, y, sdO, a.dout, qt * TILE, h, b)) break;
+          ++y;
+        } else {
+          const int head = b * a.Hkv + h / a.G;
+          for (int j = 0; j < tiles; ++j) {
+            if (!STAY || head != last_head) {
+              const uint32_t i = k_at(x, j);
+              if (!load(K_FULL + i, K_READ + i, k_uses[i], sK(i), a.k, (k0 + j) * TILE, h / a.G, b)) break;
+              ++k_uses[i];
+              ++x;
+            }
+            if (!load(V_FULL, V_READ, y, sV, a.v, (k0 + j) * TILE, h / a.G, b)) break;
+            ++y;
+          }
+          last_head = head;
         }
       }
-      if (nf > 0) mbar_wait(bar(FIXED_FULL), (nf - 1) & 1u, a.status);
-      for (uint32_t x = nk > STAGES ? nk - STAGES : 0; x < nk; ++x) mbar_wait(bar(FULL + x % STAGES), (x / STAGES) & 1u, a.status);
-      if (!ok) *k.abort_flag = 1;
+      // every copy has landed before this CTA's shared memory goes
+      if (k.warp == ROW_TMA_WARP) {
+        for (uint32_t u = x > NX ? x - NX : 0; u < x; ++u) mbar_wait(bar(Q_FULL + u % NX), (u / NX) & 1u, a.status);
+        if (y > 0) mbar_wait(bar(DO_FULL), (y - 1) & 1u, a.status);
+      } else {
+        for (int i = 0; i < 3; ++i)
+          if (k_uses[i] > 0) mbar_wait(bar(K_FULL + i), (k_uses[i] - 1) & 1u, a.status);
+        if (y > 0) mbar_wait(bar(V_FULL), (y - 1) & 1u, a.status);
+      }
     }
-  } else {
-    uint32_t nk = 0, nt = 0, ni = 0;
+  } else if (k.warp == MMA_WARP) {
+    uint32_t nt = 0, ns = 0, ni = 0;                     // tiles, items begun, items whose dQ is complete
     const uint32_t e = elect_one();
-    bool ok = true;
-    auto wait = [&](int i, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, a.status));
-      fence_after();
-      return ok;
+    // dQ += dS K of a tile
+    struct Tile { uint32_t t, k; int steps; bool first, last; };
+    auto issue_dq = [&](const Tile& p) {
+      if (!wait2(DS_FULL, p.t)) return;
+      // the accumulator is this item's once the last item's has been read
+      if (p.first && ni > 0 && !wait(ACC_READ, ni - 1)) return;
+      product_ts<D, 0>(e, k.tmem + 384u, k.tmem + 256u + 64u * (p.t & 1u), sK(p.k), p.steps, !p.first);
+      if (!STAY) mma_commit_if(e, bar(K_READ + p.k));
+      if (p.last) {
+        mma_commit_if(e, bar(ACC_FULL));
+        ++ni;
+      }
     };
-    auto wait_stage = [&](uint32_t i) { return wait(FULL + i % STAGES, (i / STAGES) & 1u); };
-    const uint32_t sQ = k.base, sdO = k.base + L::BYTES;
-    for (int it = blockIdx.x; ok && it < a.qitems; it += gridDim.x) {
+    Tile prev = {};
+    bool have = false;
+    uint32_t k_uses[2] = {0, 0};                         // copies of K that stay
+    int last_head = -1, head_tiles = 0;
+    for (int it = it0; ok && it < end; it += step) {
       int b, h, qt, k0;
       const int valid = __shfl_sync(0xffffffffu, kept(it), 0);
       const int tiles = item(it, valid, b, h, qt, k0);
       if (tiles == 0) continue;
-      const int last = valid - (k0 + tiles - 1) * TILE;
-      auto n16 = [&](int j) { return j == tiles - 1 && last < TILE ? (last + 15) & ~15 : TILE; };
-      // S of tile j: K_j's rows past the last kept key are zeroed first, up to
-      // the K of dS K_j (0 * NaN is NaN)
-      auto issue_s = [&](int j) -> bool {
-        const uint32_t i = nk + 2 * (uint32_t)j;
-        if (!wait_stage(i)) return false;
-        const int n = n16(j);
-        if (j == tiles - 1 && n > last) {
-          for (int x = k.lane; x < (n - last) * (D / 8); x += 32) {
-            const int row = last + x / (D / 8), c = x % (D / 8);
-            const uint32_t at = stage(i) + (c >> 3) * L::ATOM + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+      const int head = b * a.Hkv + h / a.G;
+      const bool fresh = !STAY || head != last_head;     // K has been copied for this item
+      if (STAY && fresh) {
+        // the last head's K is done with once its last dQ is
+        if (have) issue_dq(prev);
+        if (!ok) break;
+        have = false;
+        for (int j = 0; j < head_tiles; ++j) mma_commit_if(e, bar(K_READ + j));
+        head_tiles = tiles;
+      }
+      last_head = head;
+      for (int j = 0; ok && j < tiles; ++j, ++nt) {
+        const uint32_t ki = k_at(nt, j);
+        const bool last = j == tiles - 1;
+        const int keys = last ? valid - (k0 + j) * TILE : TILE;
+        const int n = keys < TILE ? (keys + 15) & ~15 : TILE;
+        if (j == 0 && !wait(Q_FULL + ns % NX, ns / NX)) break;
+        if (fresh && !wait(K_FULL + ki, !STAY ? nt / NK : j == 0 ? k_uses[0]++ : k_uses[1]++)) break;
+        if (fresh && n > keys) {
+          // K's rows past the last kept key are zeroed, up to the K of dS K (0 * NaN is NaN)
+          for (int x = k.lane; x < (n - keys) * (D / 8); x += 32) {
+            const int row = keys + x / (D / 8), c = x % (D / 8);
+            const uint32_t at = sK(ki) + (c >> 3) * L::ATOM + row * 128 + (((c & 7) ^ (row & 7)) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
           }
           fence_proxy_async();
           __syncwarp();
         }
-        product_nt<D>(e, k.tmem + 256u * ((nt + j) & 1u), sQ, stage(i), n);
-        mma_commit_if(e, bar(S_FULL0 + ((nt + j) & 1u)));
-        return true;
-      };
-      auto issue_dp = [&](int j) -> bool {
-        const uint32_t i = nk + 2 * (uint32_t)j + 1;
-        if (!wait_stage(i)) return false;
-        product_nt<D>(e, k.tmem + 128u, sdO, stage(i), n16(j));
+        if (nt > 0 && !wait(S_READ, nt - 1)) break;
+        product_nt<D>(e, k.tmem, sX(ns), sK(ki), n);
+        mma_commit_if(e, bar(S_FULL));
+        if (last) mma_commit_if(e, bar(Q_READ + ns % NX));
+        if (j == 0 && !wait(DO_FULL, ns)) break;
+        if (!wait(V_FULL, nt)) break;
+        if (nt > 0 && !wait(DP_READ, nt - 1)) break;
+        product_nt<D>(e, k.tmem + 128u, sdO, sV, n);
         mma_commit_if(e, bar(DP_FULL));
-        mma_commit_if(e, bar(EMPTY + i % STAGES));
-        return true;
-      };
-      if (!wait(FIXED_FULL, ni & 1u) || !issue_s(0) || !issue_dp(0)) break;
-      if (tiles > 1 && !issue_s(1)) break;
-      for (int j = 0; j < tiles; ++j) {
-        if (!wait(DS_FULL, (nt + j) & 1u)) break;
-        if (j == 0 && ni > 0 && !wait(ACC_EMPTY, (ni - 1) & 1u)) break;
-        product_ts<D>(e, k.tmem + 384u, k.tmem + 128u, stage(nk + 2 * j), n16(j) / 16, j > 0);     // dQ += dS K
-        mma_commit_if(e, bar(EMPTY + (nk + 2 * j) % STAGES));
-        if (j + 1 < tiles && !issue_dp(j + 1)) break;
-        // S buffer (nt + j) & 1 has been read: its P went into dS
-        if (j + 2 < tiles && !issue_s(j + 2)) break;
+        mma_commit_if(e, bar(V_READ));
+        if (last) mma_commit_if(e, bar(DO_READ));
+        if (have) issue_dq(prev);
+        prev = Tile{nt, ki, n / 16, j == 0, last};
+        have = true;
       }
-      if (!ok) break;
-      mma_commit_if(e, bar(FIXED_EMPTY));
-      mma_commit_if(e, bar(ACC_FULL));
-      nk += 2 * tiles;
-      nt += tiles;
-      ++ni;
+      ++ns;
     }
-    if (!ok && k.lane == 0) *k.abort_flag = 1;
+    if (ok && have) issue_dq(prev);
     mma_commit_if(e, bar(DRAIN));
     mbar_wait(bar(DRAIN), 0, a.status);
     __syncwarp();
   }
+  if (!ok) *k.abort_flag = 1;
   finish(k);
 }
 
@@ -669,6 +784,9 @@ static Plan plan(const Problem& p, Args* a) {
   const int64_t rows = (int64_t)p.B * p.Hq * a->qtiles;
   a->qsplits = (int)std::max<int64_t>(1, std::min<int64_t>(a->ktiles, SM_COUNT / rows));
   a->qitems = (int)(rows * a->qsplits);
+  a->stay = a->ktiles <= 2 && a->qsplits == 1;
+  // lengths differ between items: spread them
+  a->q_per = p.key_len == nullptr && p.key_mask == nullptr ? (a->qitems + SM_COUNT - 1) / SM_COUNT : 0;
   Plan pl;
   size_t o = 0;
   auto take = [&](size_t n) { const size_t at = o; o = align_up(o + n); return at; };
@@ -682,12 +800,13 @@ static Plan plan(const Problem& p, Args* a) {
 
 template <int D>
 static cudaError_t run(const Args& a, cudaStream_t s) {
+  const auto rows = a.stay ? rows_kernel<D, true> : rows_kernel<D, false>;
   cudaError_t e = cudaFuncSetAttribute(keys_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
   if (e != cudaSuccess) return e;
-  row_kernel<D><<<dim3(a.NqP / (256 / (D / 8)), a.B * a.Hq), 256, 0, s>>>(a);
-  keys_kernel<D><<<std::min(a.kitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
-  rows_kernel<D><<<std::min(a.qitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
+  stat_kernel<D><<<dim3((a.NqP * (D / 64) + 127) / 128, a.B * a.Hq), 256, 0, s>>>(a);
+  rows<<<std::min(a.qitems, SM_COUNT), ROWS_THREADS, Lay<D>::SMEM, s>>>(a);
+  keys_kernel<D><<<std::min(a.kitems, SM_COUNT), KEYS_THREADS, Lay<D>::SMEM, s>>>(a);
   sum_kernel<D><<<dim3((a.Nk * (D / 64) + 15) / 16, a.Hkv, a.B), 256, 0, s>>>(a);
   if (a.qsplits > 1) sum_rows_kernel<D><<<dim3((a.Nq * (D / 64) + 15) / 16, a.B * a.Hq), 256, 0, s>>>(a);
   return cudaGetLastError();
@@ -706,6 +825,7 @@ cudaError_t launch_bwd(const Problem& p, const Gradients& g, const int32_t* plac
   if (!make_tensor_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE) ||
       !make_tensor_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
       !make_tensor_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
+      !make_tensor_map(&a.dqm, g.dq, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE) ||
       !make_tensor_map(&a.dout, g.dout, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE))
     return cudaErrorInvalidValue;
   char* w = static_cast<char*>(ws);

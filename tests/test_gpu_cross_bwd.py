@@ -22,6 +22,10 @@ CASES = [
     (3, 2, 1, 257, 333, 128, "bf16", "empty"),
     (1, 2, 2, 64, 3000, 128, "bf16", "mask"),
     (2, 5, 5, 2000, 260, 64, "bf16", "none"),
+    (5, 10, 5, 900, 250, 128, "bf16", "lengths"),
+    (4, 10, 2, 900, 200, 64, "bf16", "lengths mask"),
+    (1, 40, 40, 1500, 200, 128, "bf16", "none"),
+    (1, 40, 20, 1000, 100, 64, "bf16", "none"),
     (1, 8, 2, 5000, 512, 128, "bf16", "none"),
 ]
 
