@@ -186,9 +186,15 @@ def workspace_region(p: Params, name: str):
 
 # ---------------------------------------------------------------- torch glue
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream():
@@ -373,58 +379,71 @@ def forward_host(p: Params, q_host, k_host, v_host, out_host, ws, lse_host=None)
 # x.transpose(1, 2)). All tensors of a call are on one device, the call's
 # kernels on that device's current stream.
 
+_DT = None            # torch's types by code
+
+
 def _dtype_of(code):
+    global _DT
+    if _DT is None:
+        torch = _torch()
+        _DT = (torch.bfloat16, torch.float16, torch.float32)
+    return _DT[code]
+
+
+def _wrong(t, name, dev, dtype, shape, what):
+    """The error of a tensor that is not the one asked for."""
     torch = _torch()
-    return (torch.bfloat16, torch.float16, torch.float32)[code]
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+        return TypeError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    return TypeError(f"{name} must be {what} {dtype} tensor of shape {tuple(shape)}, "
+                     f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _on(t, name, device, dtype, shape, contiguous=False):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.device != device or device.type != "cuda":
-        raise TypeError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype or tuple(t.shape) != shape or (contiguous and not t.is_contiguous()):
-        kind = "a contiguous" if contiguous else "a"
-        raise TypeError(f"{name} must be {kind} {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
+def _on(t, name, dev, dtype, shape):
+    """Address of a contiguous tensor of this device (by number), type and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise _wrong(t, name, dev, dtype, shape, "a contiguous")
 
 
-def _view(t, name, device, dtype, shape):
-    ptr = _on(t, name, device, dtype, shape)
-    b, h, n, one = t.stride()
-    if one != 1:
-        raise TypeError(f"{name}: the last axis must be contiguous")
-    return View(ptr, b, h, n)
+def _view(t, name, dev, dtype, shape):
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            b, h, n, one = t.stride()
+            if one == 1:
+                return View(t.data_ptr(), b, h, n)
+    except AttributeError:
+        pass
+    raise _wrong(t, name, dev, dtype, shape, "a (last axis contiguous)")
 
 
 def _device(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-class _Current:
-    """Makes a device current for a call where it is not."""
-
-    def __init__(self, device):
-        torch = _torch()
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _call(fn, where, dev, *args):
+    """A library call on the device's current stream, with that device current."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if code != 0:
+        raise SparkError(code, where)
 
 
-def _scratch(ws, size, device, where):
+def _scratch(ws, size, dev, where):
     torch = _torch()
     if ws is None:
-        return torch.empty(size, dtype=torch.uint8, device=device)
-    if not isinstance(ws, torch.Tensor) or ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise TypeError(f"{where}: ws must be a contiguous uint8 tensor on {device}")
+        return torch.empty(size(), dtype=torch.uint8, device=dev)
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise TypeError(f"{where}: ws must be a contiguous uint8 tensor on cuda:{dev}")
     return ws
 
 
@@ -465,10 +484,9 @@ def alloc_rotary_workspace(p: RotaryParams, device="cuda"):
 
 
 def _rotary_extras(p, device, dtype, positions, q_weight, k_weight):
-    pos = None if positions is None else _on(positions, "positions", device, _torch().float32,
-                                             (p.B, p.N, p.axes), True)
-    wq = None if q_weight is None else _on(q_weight, "q_weight", device, dtype, (p.d,), True)
-    wk = None if k_weight is None else _on(k_weight, "k_weight", device, dtype, (p.d,), True)
+    pos = None if positions is None else _on(positions, "positions", device, _dtype_of(2), (p.B, p.N, p.axes))
+    wq = None if q_weight is None else _on(q_weight, "q_weight", device, dtype, (p.d,))
+    wk = None if k_weight is None else _on(k_weight, "k_weight", device, dtype, (p.d,))
     return pos, wq, wk
 
 
@@ -493,8 +511,7 @@ def rotary(p: RotaryParams, q, k=None, positions=None, q_weight=None, k_weight=N
         qo, ko = out
     wqo = _view(qo, "q_out", dev, dt, qs)
     wko = None if k is None else _view(ko, "k_out", dev, dt, ks)
-    with _Current(dev):
-        _check(lib().spark_rotary(p, vq, vk, pos, wq, wk, wqo, wko, _stream()), "spark_rotary")
+    _call(lib().spark_rotary, "spark_rotary", dev, p, vq, vk, pos, wq, wk, wqo, wko)
     return qo, ko
 
 
@@ -521,14 +538,13 @@ def rotary_bwd(p: RotaryParams, dq_out, dk_out=None, q=None, k=None, positions=N
     dwq = None if wq is None else torch.empty(p.d, dtype=torch.float32, device=dev)
     dwk = None if wk is None or p.Hk == 0 else torch.empty(p.d, dtype=torch.float32, device=dev)
     if wq is not None or wk is not None:
-        ws = _scratch(ws, rotary_workspace_size(p), dev, "rotary_bwd")
+        ws = _scratch(ws, lambda: rotary_workspace_size(p), dev, "rotary_bwd")
     else:
         ws = None
     odq = _view(dq, "dq", dev, dt, qs)
     odk = None if dk is None else _view(dk, "dk", dev, dt, ks)
-    with _Current(dev):
-        _check(lib().spark_rotary_bwd(p, gq, gk, vq, vk, pos, wq, wk, odq, odk, _ptr(dwq), _ptr(dwk), _ptr(ws),
-                                      0 if ws is None else ws.numel(), _stream()), "spark_rotary_bwd")
+    _call(lib().spark_rotary_bwd, "spark_rotary_bwd", dev, p, gq, gk, vq, vk, pos, wq, wk, odq, odk, _ptr(dwq),
+          _ptr(dwk), _ptr(ws), 0 if ws is None else ws.numel())
     return dq, dk, dwq, dwk
 
 
@@ -558,11 +574,12 @@ def alloc_cross_workspace(p: CrossParams, bwd=False, device="cuda"):
 
 
 def _cross_masks(p, device, key_len, key_mask):
+    if key_len is None and key_mask is None:
+        return None, None
     torch = _torch()
-    if key_mask is not None and isinstance(key_mask, torch.Tensor) and key_mask.dtype == torch.bool:
-        key_mask = key_mask.view(torch.uint8)
-    kl = None if key_len is None else _on(key_len, "key_len", device, torch.int32, (p.B,), True)
-    km = None if key_mask is None else _on(key_mask, "key_mask", device, torch.uint8, (p.B, p.Nk), True)
+    kl = None if key_len is None else _on(key_len, "key_len", device, torch.int32, (p.B,))
+    kind = torch.bool if isinstance(key_mask, torch.Tensor) and key_mask.dtype == torch.bool else torch.uint8
+    km = None if key_mask is None else _on(key_mask, "key_mask", device, kind, (p.B, p.Nk))
     return kl, km
 
 
@@ -581,10 +598,9 @@ def cross_attn(p: CrossParams, q, k, v, ws=None, key_len=None, key_mask=None, re
         out = torch.empty(qs, dtype=dt, device=dev)
     vo = _view(out, "out", dev, dt, qs)
     lse = torch.empty(qs[:3], dtype=torch.float32, device=dev) if return_lse else None
-    ws = _scratch(ws, cross_workspace_size(p), dev, "cross_attn")
-    with _Current(dev):
-        _check(lib().spark_cross_attn(p, vq, vk, vv, kl, km, vo, _ptr(lse), ws.data_ptr(), ws.numel(), _stream()),
-               "spark_cross_attn")
+    ws = _scratch(ws, lambda: cross_workspace_size(p), dev, "cross_attn")
+    _call(lib().spark_cross_attn, "spark_cross_attn", dev, p, vq, vk, vv, kl, km, vo, _ptr(lse), ws.data_ptr(),
+          ws.numel())
     return (out, lse) if return_lse else out
 
 
@@ -596,14 +612,13 @@ def cross_attn_bwd(p: CrossParams, q, k, v, out, lse, dout, ws=None, key_len=Non
     qs, ks = (p.B, p.Hq, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
     views = [_view(t, n, dev, dt, s) for t, n, s in ((q, "q", qs), (k, "k", ks), (v, "v", ks), (out, "out", qs),
                                                      (dout, "dout", qs))]
-    pl = _on(lse, "lse", dev, torch.float32, qs[:3], True)
+    pl = _on(lse, "lse", dev, torch.float32, qs[:3])
     kl, km = _cross_masks(p, dev, key_len, key_mask)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     grads = [_view(t, n, dev, dt, s) for t, n, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks))]
-    ws = _scratch(ws, cross_workspace_size(p, True), dev, "cross_attn_bwd")
-    with _Current(dev):
-        _check(lib().spark_cross_attn_bwd(p, *views[:4], pl, views[4], kl, km, *grads, ws.data_ptr(), ws.numel(),
-                                          _stream()), "spark_cross_attn_bwd")
+    ws = _scratch(ws, lambda: cross_workspace_size(p, True), dev, "cross_attn_bwd")
+    _call(lib().spark_cross_attn_bwd, "spark_cross_attn_bwd", dev, p, *views[:4], pl, views[4], kl, km, *grads,
+          ws.data_ptr(), ws.numel())
     return dq, dk, dv
 
 

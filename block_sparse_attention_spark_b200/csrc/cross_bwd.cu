@@ -801,8 +801,9 @@ static Plan plan(const Problem& p, Args* a) {
 template <int D>
 static cudaError_t run(const Args& a, cudaStream_t s) {
   const auto rows = a.stay ? rows_kernel<D, true> : rows_kernel<D, false>;
-  cudaError_t e = cudaFuncSetAttribute(keys_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
+  static std::atomic<uint64_t> done[3] = {};
+  cudaError_t e = allow_shared(keys_kernel<D>, Lay<D>::SMEM, &done[0]);
+  if (e == cudaSuccess) e = allow_shared(rows, Lay<D>::SMEM, &done[a.stay ? 1 : 2]);
   if (e != cudaSuccess) return e;
   stat_kernel<D><<<dim3((a.NqP * (D / 64) + 127) / 128, a.B * a.Hq), 256, 0, s>>>(a);
   rows<<<std::min(a.qitems, SM_COUNT), ROWS_THREADS, Lay<D>::SMEM, s>>>(a);

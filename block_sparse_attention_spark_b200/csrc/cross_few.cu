@@ -304,7 +304,8 @@ static Args plan(const Problem& p, void* ws) {
 
 template <int D, bool H>
 static cudaError_t run(const Args& a, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel<D, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel<D, H>, Lay<D>::SMEM, &done);
   if (e != cudaSuccess) return e;
   kernel<D, H><<<dim3(a.tiles, a.splits, a.p.B * a.p.Hkv), THREADS, Lay<D>::SMEM, s>>>(a);
   if (a.splits > 1) join_kernel<D, H><<<dim3(a.rows, a.p.B * a.p.Hkv), D, 0, s>>>(a);

@@ -513,7 +513,8 @@ static size_t workspace(const Problem& p, const Args& a) {
 
 template <int D, bool H>
 static cudaError_t run(const Args& a, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel<D, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::SMEM);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel<D, H>, Lay<D>::SMEM, &done);
   if (e != cudaSuccess) return e;
   kernel<D, H><<<std::min(a.items, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
   if (a.splits > 1) join_kernel<D, H><<<dim3(a.G * a.tokens * (ROWS / 8), a.B * a.Hkv), 256, 0, s>>>(a);

@@ -9,11 +9,18 @@
 // A few operations per value read and written: bound by HBM. One pass: a
 // thread owns eight values (four pairs) of one token's row, forms their four
 // cosines and sines once (turns in 64 bits: position times frequency, reduced
-// to [-1/2, 1/2], then 32-bit sincospi), and walks the heads of q and of k
-// with them in registers, four rows in flight. A warp's 32 lanes hold two
-// (d = 128) or four (d = 64) rows, so the mean of squares is a shuffle over 16
-// or 8 lanes. A block holds 256 / (d / 8) tokens; heads are split over blocks
-// when tokens alone do not fill the GPU.
+// to [-1/2, 1/2], then 32-bit sincospi), and walks heads of q or of k with
+// them in registers, four rows (gradient: two) in flight. A warp's 32 lanes hold
+// two (d = 128) or four (d = 64) rows, so the mean of squares is a shuffle over
+// 16 or 8 lanes. A block holds 256 / (d / 8) tokens of one tensor; heads are
+// split over blocks when tokens alone do not fill the GPU.
+//
+// What counts is how many warps are resident: the forward kernel held to 64
+// registers (four blocks an SM) reads and writes 72,576 tokens of 80 heads
+// (bf16, d = 128) in 463 us = 6.4 TB/s, with 80 registers in 510; a software
+// pipeline of the loads (more in flight a thread, fewer warps) took 508 to 750.
+// Heads a block: for at least six blocks an SM in all (24: the angles are
+// formed for four heads at a time, 41 against 32 us at 7,110 tokens of 32 heads).
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -24,18 +31,23 @@ namespace spark {
 namespace rotary {
 
 constexpr int THREADS = 256;
-constexpr int UNROLL = 4;              // rows in flight per thread
-constexpr int BWD_BLOCKS = SM_COUNT * 4;   // most blocks of the gradient (partial sums of dw)
+constexpr int UNROLL_F = 4, UNROLL_B = 2;  // rows in flight per thread
+constexpr int BWD_BLOCKS = SM_COUNT * 6;   // blocks of the gradient where it has partial sums of dw
 
+struct Tensor {
+  View in, x, out;                     // forward: rows, -, results; gradient: of the results, rows, of the rows
+  const void* weight;
+  int H, splits, per_split;            // heads, their shares, heads per share
+  int items;                           // token tiles * splits
+};
 struct Args {
-  View q, k, qo, ko, dq, dk;           // bwd: q, k inputs; qo, ko gradients of the outputs; dq, dk written
+  Tensor t[2];                         // q, k
   const float* pos;                    // [B, N, axes] or null
-  const void *wq, *wk;
-  float* part;                         // [blocks][2][d] partial sums of dw
-  int B, Hq, Hk, N, axes;
+  float* part;                         // [blocks][d] partial sums of dw
+  int blocks_q;                        // blocks of q; the others are k's
+  int N, axes;
   int npairs;                          // R / 2
-  int tiles, splits, per_split;        // token tiles per item, head splits, heads per split
-  long items;
+  int tiles;                           // token tiles per batch item
   int grid[3];
   float eps;
   double start[3], scale[3];
@@ -120,6 +132,29 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// Turns the lane's pairs; sign -1: backwards. A pair past R / 2 is kept (not
+// multiplied by 1 and 0: its values may be infinite).
+template <int SIGN>
+__device__ __forceinline__ void turn(float* f, const float* c, const float* s, unsigned live) {
+  if (live == 15u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float u = f[2 * j], v = f[2 * j + 1], sj = SIGN * s[j];
+      f[2 * j] = fmaf(u, c[j], -v * sj);
+      f[2 * j + 1] = fmaf(u, sj, v * c[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float u = f[2 * j], v = f[2 * j + 1], sj = SIGN * s[j];
+      if ((live >> j) & 1u) {
+        f[2 * j] = fmaf(u, c[j], -v * sj);
+        f[2 * j + 1] = fmaf(u, sj, v * c[j]);
+      }
+    }
+  }
+}
+
 template <typename T, int D, int MODE, bool NORM>
 __device__ __forceinline__ void forward_row(Row<T, MODE>& x, const float* c, const float* s, const float* w,
                                             unsigned live, float eps) {
@@ -130,18 +165,11 @@ __device__ __forceinline__ void forward_row(Row<T, MODE>& x, const float* c, con
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
-    const float r = 1.f / sqrtf(row_sum<D / 8>(ss) * (1.f / D) + eps);
+    const float r = rsqrtf(row_sum<D / 8>(ss) * (1.f / D) + eps);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= r * w[j];
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float u = f[2 * j], v = f[2 * j + 1];
-    if ((live >> j) & 1u) {
-      f[2 * j] = fmaf(u, c[j], -v * s[j]);
-      f[2 * j + 1] = fmaf(u, s[j], v * c[j]);
-    }
-  }
+  turn<1>(f, c, s, live);
 #pragma unroll
   for (int j = 0; j < 8; ++j) x.v[j] = from_f<T>(f[j]);
 }
@@ -153,14 +181,7 @@ __device__ __forceinline__ void backward_row(Row<T, MODE>& y, const Row<T, MODE>
   float f[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = to_f(y.v[j]);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float u = f[2 * j], v = f[2 * j + 1];
-    if ((live >> j) & 1u) {
-      f[2 * j] = fmaf(u, c[j], v * s[j]);
-      f[2 * j + 1] = fmaf(v, c[j], -u * s[j]);
-    }
-  }
+  turn<-1>(f, c, s, live);
   if constexpr (NORM) {
     float xs[8], ss = 0.f, xg = 0.f;
 #pragma unroll
@@ -171,7 +192,7 @@ __device__ __forceinline__ void backward_row(Row<T, MODE>& y, const Row<T, MODE>
     }
     ss = row_sum<D / 8>(ss);
     xg = row_sum<D / 8>(xg);
-    const float r = 1.f / sqrtf(ss * (1.f / D) + eps);
+    const float r = rsqrtf(ss * (1.f / D) + eps);
     const float t = r * r * xg * (1.f / D);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -183,48 +204,51 @@ __device__ __forceinline__ void backward_row(Row<T, MODE>& y, const Row<T, MODE>
   for (int j = 0; j < 8; ++j) y.v[j] = from_f<T>(f[j]);
 }
 
-// The heads [h0, h1) of one tensor at one token.
+// The heads [h0, h1) of a tensor at one token.
 template <typename T, int D, int MODE, bool BWD, bool NORM>
-__device__ __forceinline__ void heads(const View& in, const View& x, const View& out, const void* weight, int b, int n,
-                                      int h0, int h1, int l, const Args& a, const float* c, const float* s,
-                                      unsigned live, bool active, float* dw) {
+__device__ __forceinline__ void heads(const Tensor& t, int b, int n, int h0, int h1, int l, int npairs, float eps,
+                                      const float* c, const float* s, unsigned live, bool active, float* dw) {
+  constexpr int UNROLL = BWD ? UNROLL_B : UNROLL_F;
   float w[8];
   if constexpr (NORM) {
     Row<T, MODE> wr;
-    wr.load(static_cast<const T*>(weight), l, a.npairs);
+    wr.load(static_cast<const T*>(t.weight), l, npairs);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = to_f(wr.v[j]);
   }
-  const T* pi = reinterpret_cast<const T*>(in.data) + b * in.b + n * in.n;
-  const T* px = BWD && NORM ? reinterpret_cast<const T*>(x.data) + b * x.b + n * x.n : nullptr;
-  T* po = reinterpret_cast<T*>(out.data) + b * out.b + n * out.n;
+  const T* pi = reinterpret_cast<const T*>(t.in.data) + b * t.in.b + n * t.in.n;
+  const T* px = BWD && NORM ? reinterpret_cast<const T*>(t.x.data) + b * t.x.b + n * t.x.n : nullptr;
+  T* po = reinterpret_cast<T*>(t.out.data) + b * t.out.b + n * t.out.n;
   int h = h0;
   for (; h + UNROLL <= h1; h += UNROLL) {
     Row<T, MODE> r[UNROLL], rx[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      r[u].load(pi + (h + u) * in.h, l, a.npairs);
-      if constexpr (BWD && NORM) rx[u].load(px + (h + u) * x.h, l, a.npairs);
+      r[u].load(pi + (h + u) * t.in.h, l, npairs);
+      if constexpr (BWD && NORM) rx[u].load(px + (h + u) * t.x.h, l, npairs);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      if constexpr (BWD) backward_row<T, D, MODE, NORM>(r[u], rx[u], c, s, w, live, a.eps, active, dw);
-      else forward_row<T, D, MODE, NORM>(r[u], c, s, w, live, a.eps);
-      if (active) r[u].store(po + (h + u) * out.h, l, a.npairs);
+      if constexpr (BWD) backward_row<T, D, MODE, NORM>(r[u], rx[u], c, s, w, live, eps, active, dw);
+      else forward_row<T, D, MODE, NORM>(r[u], c, s, w, live, eps);
+      if (active) r[u].store(po + (h + u) * t.out.h, l, npairs);
     }
   }
   for (; h < h1; ++h) {
     Row<T, MODE> r, rx;
-    r.load(pi + h * in.h, l, a.npairs);
-    if constexpr (BWD && NORM) rx.load(px + h * x.h, l, a.npairs);
-    if constexpr (BWD) backward_row<T, D, MODE, NORM>(r, rx, c, s, w, live, a.eps, active, dw);
-    else forward_row<T, D, MODE, NORM>(r, c, s, w, live, a.eps);
-    if (active) r.store(po + h * out.h, l, a.npairs);
+    r.load(pi + h * t.in.h, l, npairs);
+    if constexpr (BWD && NORM) rx.load(px + h * t.x.h, l, npairs);
+    if constexpr (BWD) backward_row<T, D, MODE, NORM>(r, rx, c, s, w, live, eps, active, dw);
+    else forward_row<T, D, MODE, NORM>(r, c, s, w, live, eps);
+    if (active) r.store(po + h * t.out.h, l, npairs);
   }
 }
 
-template <typename T, int D, int MODE, bool BWD>
-__global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a) {
+// NORMED: some tensor has a weight. Blocks an SM: the gradient without a norm at
+// four (64 registers; 40 + 40 heads of 36,288 tokens 254 us, at three 286), with
+// one at three (at four it spills: 117 against 94 us for 16 heads of 32,256).
+template <typename T, int D, int MODE, bool BWD, bool NORMED>
+__global__ void __launch_bounds__(THREADS, BWD && NORMED ? 3 : 4) kernel(const __grid_constant__ Args a) {
   constexpr int LPR = D / 8, TOK = THREADS / LPR;
   __shared__ double freq[64];
   __shared__ unsigned char axis[64];
@@ -234,14 +258,15 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
     axis[tid] = a.axis[tid];
   }
   __syncthreads();
-  float dwq[8], dwk[8];
+  const bool second = (int)blockIdx.x >= a.blocks_q;
+  const Tensor& t = a.t[second];
+  const int first = blockIdx.x - (second ? a.blocks_q : 0), step = second ? gridDim.x - a.blocks_q : a.blocks_q;
+  float dw[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dwq[j] = dwk[j] = 0.f;
-  for (long it = blockIdx.x; it < a.items; it += gridDim.x) {
-    const int split = (int)(it % a.splits);
-    const long tile = it / a.splits;
-    const int b = (int)(tile / a.tiles);
-    const int tok = (int)(tile % a.tiles) * TOK + tid / LPR;
+  for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+  for (int it = first; it < t.items; it += step) {
+    const int split = it % t.splits, tile = it / t.splits;
+    const int b = tile / a.tiles, tok = (tile % a.tiles) * TOK + tid / LPR;
     const bool active = tok < a.N;
     const int n = active ? tok : a.N - 1;              // idle lanes follow the last token, unwritten
     // this lane's four angles
@@ -276,67 +301,53 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
         sincospif((float)(2.0 * t), &s[j], &c[j]);
       }
     }
-    const int h0 = split * a.per_split, h1 = min(h0 + a.per_split, a.Hq + a.Hk);
-    if (h0 < a.Hq) {
-      if (a.wq != nullptr)
-        heads<T, D, MODE, BWD, true>(BWD ? a.qo : a.q, a.q, BWD ? a.dq : a.qo, a.wq, b, n, h0, min(h1, a.Hq), l, a, c,
-                                     s, live, active, dwq);
-      else
-        heads<T, D, MODE, BWD, false>(BWD ? a.qo : a.q, a.q, BWD ? a.dq : a.qo, nullptr, b, n, h0, min(h1, a.Hq), l, a,
-                                      c, s, live, active, dwq);
-    }
-    if (h1 > a.Hq) {
-      if (a.wk != nullptr)
-        heads<T, D, MODE, BWD, true>(BWD ? a.ko : a.k, a.k, BWD ? a.dk : a.ko, a.wk, b, n, max(h0, a.Hq) - a.Hq,
-                                     h1 - a.Hq, l, a, c, s, live, active, dwk);
-      else
-        heads<T, D, MODE, BWD, false>(BWD ? a.ko : a.k, a.k, BWD ? a.dk : a.ko, nullptr, b, n, max(h0, a.Hq) - a.Hq,
-                                      h1 - a.Hq, l, a, c, s, live, active, dwk);
-    }
+    const int h0 = split * t.per_split, h1 = min(h0 + t.per_split, t.H);
+    if (NORMED && t.weight != nullptr)
+      heads<T, D, MODE, BWD, NORMED>(t, b, n, h0, h1, l, a.npairs, a.eps, c, s, live, active, dw);
+    else
+      heads<T, D, MODE, BWD, false>(t, b, n, h0, h1, l, a.npairs, a.eps, c, s, live, active, dw);
   }
-  if constexpr (BWD) {
+  if constexpr (BWD && NORMED) {
     // this block's sums of dw: tokens of a warp by shuffles, warps in shared memory, a fixed order
-    if (a.wq == nullptr && a.wk == nullptr) return;
-    __shared__ float sh[2][THREADS / 32][D];
+    if (t.weight == nullptr) return;
+    __shared__ float sh[THREADS / 32][D];
     const int warp = tid >> 5, lane = tid & 31;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) {
-        dwq[j] += __shfl_xor_sync(0xffffffffu, dwq[j], o);
-        dwk[j] += __shfl_xor_sync(0xffffffffu, dwk[j], o);
-      }
-      if (lane < LPR) {
-        const int i = Row<T, MODE>::at(l, j, a.npairs);
-        sh[0][warp][i] = dwq[j];
-        sh[1][warp][i] = dwk[j];
-      }
+      for (int o = LPR; o < 32; o <<= 1) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], o);
+      if (lane < LPR) sh[warp][Row<T, MODE>::at(l, j, a.npairs)] = dw[j];
     }
     __syncthreads();
-    for (int i = tid; i < 2 * D; i += THREADS) {
+    if (tid < D) {
       float v = 0.f;
 #pragma unroll
-      for (int x = 0; x < THREADS / 32; ++x) v += sh[i / D][x][i % D];
-      a.part[(size_t)blockIdx.x * 2 * D + i] = v;
+      for (int x = 0; x < THREADS / 32; ++x) v += sh[x][tid];
+      a.part[(size_t)blockIdx.x * D + tid] = v;
     }
   }
 }
 
-// dw of both tensors: the blocks' partial sums, 32 columns per block, in 64 bits.
-__global__ void __launch_bounds__(1024) sum_kernel(const float* __restrict__ part, int blocks, int d,
-                                                   float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ double sh[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + x;
+// dw of q (blockIdx.y 0) and of k: the blocks' partial sums, eight columns a
+// block, in 64 bits and a fixed order.
+__global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ part, int blocks_q, int blocks, int d,
+                                                  float* __restrict__ dwq, float* __restrict__ dwk) {
+  __shared__ double sh[32][9];
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int col = blockIdx.x * 8 + x;
+  float* dst = blockIdx.y ? dwk : dwq;
+  if (dst == nullptr) return;
+  const int b0 = blockIdx.y ? blocks_q : 0, b1 = blockIdx.y ? blocks : blocks_q;
   double v = 0.0;
-  for (int i = y; i < blocks; i += 32) v += (double)part[(size_t)i * 2 * d + col];
+#pragma unroll 8
+  for (int i = b0 + y; i < b1; i += 32) v += (double)part[(size_t)i * d + col];
   sh[y][x] = v;
   __syncthreads();
   if (y == 0) {
     double t = 0.0;
+#pragma unroll
     for (int i = 0; i < 32; ++i) t += sh[i][x];
-    float* dst = col < d ? dwq : dwk;
-    if (dst != nullptr) dst[col < d ? col : col - d] = (float)t;
+    dst[col] = (float)t;
   }
 }
 
@@ -372,59 +383,69 @@ static bool grid_fits(const spark_rotary_params* p) {
 }
 
 // Frequencies and the split of the work; the pointers are filled in by the calls.
-static Args plan(const spark_rotary_params* p, const float* pos) {
+static Args plan(const spark_rotary_params* p, const float* pos, bool bwd) {
   Args a = {};
-  a.B = p->B; a.Hq = p->Hq; a.Hk = p->Hk; a.N = p->N; a.axes = p->axes;
+  a.N = p->N;
+  a.axes = p->axes;
   a.pos = pos;
   a.eps = (float)p->eps;
   int R = 0;
   for (int x = 0; x < p->axes; ++x) R += p->dims[x];
   a.npairs = R / 2;
   a.grid[0] = a.grid[1] = a.grid[2] = 1;
+  double f = 1.0 / 6.283185307179586476925;
   for (int x = 0, i = 0; x < p->axes; ++x) {
     if (pos == nullptr) a.grid[x] = p->grid[x];
     a.start[x] = p->start[x];
     a.scale[x] = p->scale[x];
-    for (int j = 0; j < p->dims[x] / 2; ++j, ++i) {
-      const double e = p->spectrum == SPARK_ROTARY_PER_AXIS ? 2.0 * j / p->dims[x] : 2.0 * i / R;
-      a.freq[i] = pow(p->theta, -e) / 6.283185307179586476925;
+    // theta^(-2j / n) by steps of theta^(-2 / n): 64 roundings of 2^-53 at most
+    const double step = p->dims[x] > 0 ? pow(p->theta, -2.0 / (p->spectrum == SPARK_ROTARY_PER_AXIS ? p->dims[x] : R)) : 1.0;
+    if (p->spectrum == SPARK_ROTARY_PER_AXIS) f = 1.0 / 6.283185307179586476925;
+    for (int j = 0; j < p->dims[x] / 2; ++j, ++i, f *= step) {
+      a.freq[i] = f;
       a.axis[i] = (unsigned char)x;
     }
   }
-  const int tok = THREADS / (p->d / 8), heads = p->Hq + p->Hk;
+  // heads per block: they share a token's angles, so as many as still give every
+  // SM a few blocks
+  const int tok = THREADS / (p->d / 8), unroll = bwd ? UNROLL_B : UNROLL_F;
   a.tiles = (p->N + tok - 1) / tok;
-  // heads per block: all of them share a token's angles, so as many as still
-  // give every SM several blocks
-  const long tiles = (long)a.tiles * p->B;
-  const long want = (long)SM_COUNT * 24;
-  int splits = (int)std::min<long>((heads + UNROLL - 1) / UNROLL, std::max<long>(1, (want + tiles - 1) / tiles));
-  a.per_split = ((heads + splits - 1) / splits + UNROLL - 1) / UNROLL * UNROLL;
-  a.splits = (heads + a.per_split - 1) / a.per_split;
-  a.items = tiles * a.splits;
+  const int64_t tiles = (int64_t)a.tiles * p->B, want = SM_COUNT * 6;
+  const int heads = p->Hq + p->Hk;
+  const int64_t share = std::max<int64_t>(1, tiles * heads / want);      // heads a block, for `want` blocks in all
+  for (int x = 0; x < 2; ++x) {
+    Tensor& t = a.t[x];
+    t.H = x ? p->Hk : p->Hq;
+    if (t.H == 0) continue;
+    t.per_split = (int)std::min<int64_t>(t.H, (share + unroll - 1) / unroll * unroll);
+    t.splits = (t.H + t.per_split - 1) / t.per_split;
+    t.per_split = (t.H + t.splits - 1) / t.splits;
+    t.items = (int)std::min<int64_t>(tiles * t.splits, INT32_MAX);
+  }
   return a;
 }
 
-template <typename T, int D, bool BWD>
+template <typename T, int D, bool BWD, bool NORMED>
 static void launch_mode(int mode, int blocks, const Args& a, cudaStream_t s) {
-  if (mode == CONTIG) kernel<T, D, CONTIG, BWD><<<blocks, THREADS, 0, s>>>(a);
-  else if (mode == SPLIT4) kernel<T, D, SPLIT4, BWD><<<blocks, THREADS, 0, s>>>(a);
-  else kernel<T, D, SINGLES, BWD><<<blocks, THREADS, 0, s>>>(a);
+  if (mode == CONTIG) kernel<T, D, CONTIG, BWD, NORMED><<<blocks, THREADS, 0, s>>>(a);
+  else if (mode == SPLIT4) kernel<T, D, SPLIT4, BWD, NORMED><<<blocks, THREADS, 0, s>>>(a);
+  else kernel<T, D, SINGLES, BWD, NORMED><<<blocks, THREADS, 0, s>>>(a);
 }
 
-template <bool BWD>
-static spark_status launch(const spark_rotary_params* p, int blocks, const Args& a, cudaStream_t s) {
+template <typename T, bool BWD, bool NORMED>
+static void launch_size(const spark_rotary_params* p, int blocks, const Args& a, cudaStream_t s) {
   // half-split pairs: four of them per lane as two 4-value copies when R is a
   // multiple of 8, else value by value
   const int mode = p->pairing == SPARK_ROTARY_INTERLEAVED ? CONTIG : (a.npairs % 4 == 0 ? SPLIT4 : SINGLES);
-  if (p->d == 128) {
-    if (p->dtype == SPARK_BF16) launch_mode<__nv_bfloat16, 128, BWD>(mode, blocks, a, s);
-    else if (p->dtype == SPARK_FP16) launch_mode<__half, 128, BWD>(mode, blocks, a, s);
-    else launch_mode<float, 128, BWD>(mode, blocks, a, s);
-  } else {
-    if (p->dtype == SPARK_BF16) launch_mode<__nv_bfloat16, 64, BWD>(mode, blocks, a, s);
-    else if (p->dtype == SPARK_FP16) launch_mode<__half, 64, BWD>(mode, blocks, a, s);
-    else launch_mode<float, 64, BWD>(mode, blocks, a, s);
-  }
+  if (p->d == 128) launch_mode<T, 128, BWD, NORMED>(mode, blocks, a, s);
+  else launch_mode<T, 64, BWD, NORMED>(mode, blocks, a, s);
+}
+
+template <bool BWD, bool NORMED>
+static spark_status launch(const spark_rotary_params* p, int blocks, const Args& a, cudaStream_t s) {
+  if (p->dtype == SPARK_BF16) launch_size<__nv_bfloat16, BWD, NORMED>(p, blocks, a, s);
+  else if (p->dtype == SPARK_FP16) launch_size<__half, BWD, NORMED>(p, blocks, a, s);
+  else launch_size<float, BWD, NORMED>(p, blocks, a, s);
   return cudaGetLastError() == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
@@ -438,7 +459,7 @@ extern "C" {
 spark_status spark_rotary_validate(const spark_rotary_params* p) { return rotary::validate(p); }
 
 size_t spark_rotary_workspace_size(const spark_rotary_params* p) {
-  return rotary::validate(p) == SPARK_OK ? (size_t)rotary::BWD_BLOCKS * 2 * p->d * sizeof(float) : 0;
+  return rotary::validate(p) == SPARK_OK ? (size_t)rotary::BWD_BLOCKS * p->d * sizeof(float) : 0;
 }
 
 spark_status spark_rotary(const spark_rotary_params* p, const spark_view* q, const spark_view* k,
@@ -447,19 +468,21 @@ spark_status spark_rotary(const spark_rotary_params* p, const spark_view* q, con
   const spark_status v = rotary::validate(p);
   if (v != SPARK_OK) return v;
   if (positions == nullptr && !rotary::grid_fits(p)) return SPARK_ERR_INVALID_ARG;
-  rotary::Args a = rotary::plan(p, positions);
+  rotary::Args a = rotary::plan(p, positions, false);
   const int es = rotary::elem(p);
-  if (!make_view(q, p->B, p->Hq, p->N, p->d, es, false, &a.q) ||
-      !make_view(q_out, p->B, p->Hq, p->N, p->d, es, true, &a.qo))
+  if (!make_view(q, p->B, p->Hq, p->N, p->d, es, false, &a.t[0].in) ||
+      !make_view(q_out, p->B, p->Hq, p->N, p->d, es, true, &a.t[0].out))
     return SPARK_ERR_INVALID_ARG;
-  if (p->Hk > 0 && (!make_view(k, p->B, p->Hk, p->N, p->d, es, false, &a.k) ||
-                    !make_view(k_out, p->B, p->Hk, p->N, p->d, es, true, &a.ko)))
+  if (p->Hk > 0 && (!make_view(k, p->B, p->Hk, p->N, p->d, es, false, &a.t[1].in) ||
+                    !make_view(k_out, p->B, p->Hk, p->N, p->d, es, true, &a.t[1].out)))
     return SPARK_ERR_INVALID_ARG;
   if (!aligned(q_weight) || !aligned(k_weight) || ((uintptr_t)positions & 3u) != 0) return SPARK_ERR_INVALID_ARG;
-  if (a.items > INT32_MAX) return SPARK_ERR_UNSUPPORTED;
-  a.wq = q_weight;
-  a.wk = p->Hk > 0 ? k_weight : nullptr;
-  return rotary::launch<false>(p, (int)a.items, a, stream);
+  const int64_t blocks = (int64_t)a.t[0].items + a.t[1].items;
+  if (blocks >= INT32_MAX) return SPARK_ERR_UNSUPPORTED;
+  a.blocks_q = a.t[0].items;
+  a.t[0].weight = q_weight;
+  a.t[1].weight = k_weight;
+  return rotary::launch<false, true>(p, (int)blocks, a, stream);
 }
 
 spark_status spark_rotary_bwd(const spark_rotary_params* p, const spark_view* dq_out, const spark_view* dk_out,
@@ -470,33 +493,44 @@ spark_status spark_rotary_bwd(const spark_rotary_params* p, const spark_view* dq
   const spark_status v = rotary::validate(p);
   if (v != SPARK_OK) return v;
   if (positions == nullptr && !rotary::grid_fits(p)) return SPARK_ERR_INVALID_ARG;
-  rotary::Args a = rotary::plan(p, positions);
+  rotary::Args a = rotary::plan(p, positions, true);
   const int es = rotary::elem(p);
-  a.wq = q_weight;
-  a.wk = p->Hk > 0 ? k_weight : nullptr;
-  if (!make_view(dq_out, p->B, p->Hq, p->N, p->d, es, false, &a.qo) ||
-      !make_view(dq, p->B, p->Hq, p->N, p->d, es, true, &a.dq) ||
-      (a.wq != nullptr && !make_view(q, p->B, p->Hq, p->N, p->d, es, false, &a.q)))
-    return SPARK_ERR_INVALID_ARG;
-  if (p->Hk > 0 && (!make_view(dk_out, p->B, p->Hk, p->N, p->d, es, false, &a.ko) ||
-                    !make_view(dk, p->B, p->Hk, p->N, p->d, es, true, &a.dk) ||
-                    (a.wk != nullptr && !make_view(k, p->B, p->Hk, p->N, p->d, es, false, &a.k))))
-    return SPARK_ERR_INVALID_ARG;
+  const spark_view* views[2][3] = {{dq_out, q, dq}, {dk_out, k, dk}};
+  const void* weights[2] = {q_weight, p->Hk > 0 ? k_weight : nullptr};
+  for (int x = 0; x < (p->Hk > 0 ? 2 : 1); ++x) {
+    rotary::Tensor& t = a.t[x];
+    t.weight = weights[x];
+    if (!make_view(views[x][0], p->B, t.H, p->N, p->d, es, false, &t.in) ||
+        !make_view(views[x][2], p->B, t.H, p->N, p->d, es, true, &t.out) ||
+        (t.weight != nullptr && !make_view(views[x][1], p->B, t.H, p->N, p->d, es, false, &t.x)))
+      return SPARK_ERR_INVALID_ARG;
+  }
   if (!aligned(q_weight) || !aligned(k_weight) || ((uintptr_t)positions & 3u) != 0) return SPARK_ERR_INVALID_ARG;
-  if ((a.wq != nullptr && dq_weight == nullptr) || (a.wk != nullptr && dk_weight == nullptr))
+  if ((weights[0] != nullptr && dq_weight == nullptr) || (weights[1] != nullptr && dk_weight == nullptr))
     return SPARK_ERR_INVALID_ARG;
-  int blocks = (int)std::min<long>(a.items, INT32_MAX);
-  const bool norm = a.wq != nullptr || a.wk != nullptr;
+  const bool norm = weights[0] != nullptr || weights[1] != nullptr;
+  int64_t blocks = (int64_t)a.t[0].items + a.t[1].items;
+  if (blocks >= INT32_MAX) return SPARK_ERR_UNSUPPORTED;
+  a.blocks_q = a.t[0].items;
   if (norm) {
     if (ws == nullptr || !aligned(ws)) return SPARK_ERR_INVALID_ARG;
     if (ws_bytes < spark_rotary_workspace_size(p)) return SPARK_ERR_WORKSPACE;
     a.part = static_cast<float*>(ws);
-    blocks = (int)std::min<long>(a.items, rotary::BWD_BLOCKS);
+    // blocks in proportion to the tensors' work: a row with a norm reads its x too
+    if (blocks > rotary::BWD_BLOCKS) {
+      blocks = rotary::BWD_BLOCKS;
+      const double wq = a.t[0].H * (weights[0] ? 3.0 : 2.0), wk = a.t[1].H * (weights[1] ? 3.0 : 2.0);
+      a.blocks_q = std::min(a.t[0].items, std::max(1, (int)(blocks * wq / (wq + wk) + 0.5)));
+      if (p->Hk > 0) a.blocks_q = std::min<int>(a.blocks_q, (int)blocks - 1);
+      else a.blocks_q = (int)blocks;
+    }
   }
-  const spark_status e = rotary::launch<true>(p, blocks, a, stream);
+  const spark_status e = norm ? rotary::launch<true, true>(p, (int)blocks, a, stream)
+                              : rotary::launch<true, false>(p, (int)blocks, a, stream);
   if (e != SPARK_OK || !norm) return e;
-  rotary::sum_kernel<<<2 * p->d / 32, 1024, 0, stream>>>(a.part, blocks, p->d, a.wq ? dq_weight : nullptr,
-                                                         a.wk ? dk_weight : nullptr);
+  rotary::sum_kernel<<<dim3(p->d / 8, 2), 256, 0, stream>>>(a.part, a.blocks_q, (int)blocks, p->d,
+                                                            weights[0] ? dq_weight : nullptr,
+                                                            weights[1] ? dk_weight : nullptr);
   return cudaGetLastError() == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 

@@ -2,9 +2,11 @@
 // checks of the views a caller passes, and what the kernels get of them.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "spark.h"
 
@@ -46,6 +48,20 @@ inline bool make_view(const spark_view* v, int B, int H, int N, int d, int elem,
   out->h = str[1];
   out->n = str[2];
   return true;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, asked of the runtime once
+// per device (done: bits by device number, one word per kernel).
+template <typename F>
+inline cudaError_t allow_shared(F* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (bit != 0 && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // The library's device status word on the current device (spark_get_status).
