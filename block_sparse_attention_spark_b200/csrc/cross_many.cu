@@ -176,16 +176,85 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         ++ns;
         if (!ok) break;
         fence_after();
+        // moves the row's reference to mt, and its O and sum with it, if it has none or mt passes it
+        auto move = [&](float mt) {
+          float corr = 1.f;
+          if (m == -INFINITY) {
+            m = mt;
+          } else if (mt > m + LAZY) {
+            corr = ex2(m - mt);
+            l *= corr;
+            m = mt;
+          }
+          if (__any_sync(0xffffffffu, corr != 1.f)) {
+            // P_{j-1} V_{j-1} is done (S_j came after it), P_j V_j not issued yet
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              tmem_ld32p(oc + 32u * cc, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st32p(oc + 32u * cc, o);
+            }
+          }
+        };
+        auto hand_over = [&](int hf) {
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(s, hf));   // the MMAs of these 64 keys need not wait for the others
+        };
+        const int valid = w.valid - (w.k0 + j) * KEYS;
+        if (valid < KEYS) {
+          // an item's last tile: 32 keys at a time, only as far as the MMAs go (two passes
+          // over S; P of keys 32 c.. goes to columns 16 c.., whose S has been read)
+          const int chunks = (((valid + 15) & ~15) + 31) / 32;
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t x[32];
+            tmem_ld32p(sc + 32u * c, x);
+            tmem_ld_wait();
+            const int left = valid - 32 * c;
+            if (left >= 32) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) mt = max3(mt, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < left) mt = fmaxf(mt, __uint_as_float(x[e]));
+            }
+          }
+          move(mt * a.sl2);
+          const float ref = m == -INFINITY ? 0.f : m;        // logits all -inf: exp2(-inf - 0) = 0
+          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t x[32], pw[16];
+            tmem_ld32p(sc + 32u * c, x);
+            tmem_ld_wait();
+            const int left = valid - 32 * c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float u = ex2(fmaf(__uint_as_float(x[e]), a.sl2, -ref));
+              if (e >= left) u = 0.f;
+              x[e] = __float_as_uint(u);
+              rs[e & 3] += u;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pw[e] = pack2<H>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+            tmem_st16p(sc + 16u * c, pw);
+          }
+          l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+          hand_over(0);
+          if (lane == 0) mbar_arrive(p_full(s, 1));
+          continue;
+        }
         uint32_t sv[KEYS];
 #pragma unroll
         for (int c = 0; c < KEYS / 32; ++c) tmem_ld32p(sc + 32u * c, sv + 32 * c);
         tmem_ld_wait();
-        const int valid = w.valid - (w.k0 + j) * KEYS;
-        if (valid < KEYS) {
-#pragma unroll
-          for (int c = 0; c < KEYS; ++c)
-            if (c >= valid) sv[c] = 0xff800000u;           // -inf
-        }
         float mc[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) mc[i] = fmaxf(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
@@ -194,31 +263,9 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             mc[i] = max3(mc[i], __uint_as_float(sv[c + 2 * i]), __uint_as_float(sv[c + 2 * i + 1]));
-        const float mt = fmaxf(fmaxf(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5])), fmaxf(mc[6], mc[7])) * a.sl2;
-        float m_new = m, corr = 1.f;
-        bool resc = false;
-        if (m == -INFINITY) {
-          m_new = mt;
-        } else if (mt > m + LAZY) {
-          m_new = mt;
-          corr = ex2(m - mt);
-          resc = true;
-        }
-        if (__any_sync(0xffffffffu, resc)) {
-          // P_{j-1} V_{j-1} is done (S_j came after it), P_j V_j not issued yet
-#pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
-            tmem_ld32p(oc + 32u * cc, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st32p(oc + 32u * cc, o);
-          }
-        }
-        // a row whose logits are all -inf so far: exp2(-inf - 0) = 0 (no branch here:
-        // the stores below are collective, and rows of a warp may differ in this)
-        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        move(fmaxf(fmaxf(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5])), fmaxf(mc[6], mc[7])) * a.sl2);
+        // (no branch on a row's reference: the stores are collective, and rows of a warp may differ in it)
+        const float ref = m == -INFINITY ? 0.f : m;
         const uint64_t nm2 = f2(-ref, -ref);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -234,17 +281,12 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
             pw[c >> 1] = pack2<H>(u0, u1);
           }
           tmem_st32p(sc + 32u * hf, pw);
-          // the MMAs of these 64 keys need not wait for the others
-          tmem_st_wait();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(s, hf));
+          hand_over(hf);
         }
         float r0, r1, r2, r3;
         unf2(fadd2(acc[0], acc[1]), r0, r1);
         unf2(fadd2(acc[2], acc[3]), r2, r3);
-        l = l * corr + ((r0 + r2) + (r1 + r3));
-        m = m_new;
+        l += (r0 + r2) + (r1 + r3);
       }
       if (!ok) break;
       // for the output warps, once they have the last item's
