@@ -505,8 +505,8 @@ def rotary(p: RotaryParams, q, k=None, positions=None, q_weight=None, k_weight=N
     vk = None if k is None else _view(k, "k", dev, dt, ks)
     pos, wq, wk = _rotary_extras(p, dev, dt, positions, q_weight, k_weight)
     if out is None:
-        qo = torch.empty(qs, dtype=dt, device=dev)
-        ko = None if k is None else torch.empty(ks, dtype=dt, device=dev)
+        qo = q.new_empty(qs)
+        ko = None if k is None else k.new_empty(ks)
     else:
         qo, ko = out
     wqo = _view(qo, "q_out", dev, dt, qs)
@@ -595,9 +595,9 @@ def cross_attn(p: CrossParams, q, k, v, ws=None, key_len=None, key_mask=None, re
     vq, vk, vv = _view(q, "q", dev, dt, qs), _view(k, "k", dev, dt, ks), _view(v, "v", dev, dt, ks)
     kl, km = _cross_masks(p, dev, key_len, key_mask)
     if out is None:
-        out = torch.empty(qs, dtype=dt, device=dev)
+        out = q.new_empty(qs)
     vo = _view(out, "out", dev, dt, qs)
-    lse = torch.empty(qs[:3], dtype=torch.float32, device=dev) if return_lse else None
+    lse = q.new_empty(qs[:3], dtype=_dtype_of(2)) if return_lse else None
     ws = _scratch(ws, lambda: cross_workspace_size(p), dev, "cross_attn")
     _call(lib().spark_cross_attn, "spark_cross_attn", dev, p, vq, vk, vv, kl, km, vo, _ptr(lse), ws.data_ptr(),
           ws.numel())
@@ -612,7 +612,7 @@ def cross_attn_bwd(p: CrossParams, q, k, v, out, lse, dout, ws=None, key_len=Non
     qs, ks = (p.B, p.Hq, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
     views = [_view(t, n, dev, dt, s) for t, n, s in ((q, "q", qs), (k, "k", ks), (v, "v", ks), (out, "out", qs),
                                                      (dout, "dout", qs))]
-    pl = _on(lse, "lse", dev, torch.float32, qs[:3])
+    pl = _on(lse, "lse", dev, _dtype_of(2), qs[:3])
     kl, km = _cross_masks(p, dev, key_len, key_mask)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     grads = [_view(t, n, dev, dt, s) for t, n, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks))]

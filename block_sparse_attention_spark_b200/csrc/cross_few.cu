@@ -7,8 +7,12 @@
 // through a ring of their own in shared memory (cp.async, no block barrier in
 // the loop): 16 KB per step at d = 128, two steps in flight per warp. Each warp keeps
 // the running maximum, sum and O of its keys; warps are joined in shared
-// memory, blocks by join_kernel. Keys that are not kept are not read at all:
-// cp.async fills their rows with zeros and their logits are -inf.
+// memory. Up to eight blocks of a tile form a cluster and join over its shared
+// memory, each a part of the rows' values; more (fewer than 19 tiles on the
+// whole GPU) leave their shares in the workspace for join_kernel. Keys that are
+// not kept are not read at all: cp.async fills their rows with zeros and their
+// logits are -inf.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -21,11 +25,13 @@ namespace few {
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int ROWS = 16, KEYS = 32, STAGES = 3;
 constexpr int MIN_KEYS = WARPS * KEYS;       // fewest keys worth a block of their own
+constexpr int CLUSTER = 8;                   // most blocks of a tile that join among themselves
 
 struct Args {
   Problem p;
   int rows;                // G * Nq
   int tiles, splits;
+  int stages;              // STAGES, or 1 where a warp has one step at most
   int per_split;           // keys per split, a multiple of KEYS
   float* part;             // [tiles * B * Hkv][splits][16][d], then the (max, sum) pairs
   float2* stat;
@@ -36,8 +42,7 @@ struct Lay {
   static constexpr int ROW = 2 * D;                       // bytes of a row
   static constexpr int Q = ROWS * ROW;
   static constexpr int TILE = KEYS * ROW;                 // of K or V
-  static constexpr int WARP = STAGES * 2 * TILE;
-  static constexpr int SMEM = Q + WARPS * WARP;
+  static constexpr int smem(int stages) { return Q + WARPS * stages * 2 * TILE; }
 };
 
 // byte offset of 16-byte chunk c of row r: chunks XORed by the row, so that
@@ -91,7 +96,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile = blockIdx.x, split = blockIdx.y, bk = blockIdx.z;
   const int b = bk / p.Hkv, hk = bk % p.Hkv;
-  const uint32_t sq = smem_u32(smem), ring = sq + L::Q + warp * L::WARP;
+  const uint32_t sq = smem_u32(smem), ring = sq + L::Q + warp * a.stages * 2 * L::TILE;
   const int len = item_len(p.key_len, p.Nk, b, p.status, tid == 0 && tile == 0 && split == 0 && hk == 0);
   const int k_end = min(len, (split + 1) * a.per_split);
 
@@ -112,6 +117,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
   const int first = split * a.per_split + warp * KEYS;
   const int steps = k_end > first ? (k_end - first + MIN_KEYS - 1) / MIN_KEYS : 0;
   // issues the copies of step i; the bits of its kept keys
+  auto stage_of = [&](int i) { return a.stages == STAGES ? i % STAGES : 0; };
   auto issue = [&](int i) -> uint32_t {
     uint32_t kept = 0;
     if (i < steps) {
@@ -119,7 +125,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
       const int j = k0 + lane;
       const bool take = j < k_end && (mask == nullptr || mask[j] != 0);
       kept = __ballot_sync(0xffffffffu, take);
-      const uint32_t st = ring + (i % STAGES) * 2 * L::TILE;
+      const uint32_t st = ring + stage_of(i) * 2 * L::TILE;
 #pragma unroll
       for (int x = 0; x < CH; ++x) {
         const int e = x * 32 + lane, r = e / CH, c = e % CH;
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
     const uint32_t kept2 = issue(i + 2);
     cp_async_wait<2>();
     __syncwarp();
-    const uint32_t st = ring + (i % STAGES) * 2 * L::TILE;
+    const uint32_t st = ring + stage_of(i) * 2 * L::TILE;
     float s[KEYS / 8][4];
 #pragma unroll
     for (int n = 0; n < KEYS / 8; ++n)
@@ -226,40 +232,96 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
   float* so = reinterpret_cast<float*>(smem);                           // [WARPS][ROWS][D]
   float2* ss = reinterpret_cast<float2*>(smem + WARPS * ROWS * D * 4);  // [WARPS][ROWS]
   const int r0 = lane >> 2;
+  const int live = min(ROWS, a.rows - tile * ROWS);                     // rows of this tile
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) {
     const int c = 8 * n + 2 * (lane & 3);
-    *reinterpret_cast<float2*>(so + ((warp * ROWS + r0) * D + c)) = make_float2(o[n][0], o[n][1]);
-    *reinterpret_cast<float2*>(so + ((warp * ROWS + r0 + 8) * D + c)) = make_float2(o[n][2], o[n][3]);
+    if (r0 < live) *reinterpret_cast<float2*>(so + ((warp * ROWS + r0) * D + c)) = make_float2(o[n][0], o[n][1]);
+    if (r0 + 8 < live) *reinterpret_cast<float2*>(so + ((warp * ROWS + r0 + 8) * D + c)) = make_float2(o[n][2], o[n][3]);
   }
   if ((lane & 3) == 0) {
     ss[warp * ROWS + r0] = make_float2(m[0], l[0]);
     ss[warp * ROWS + r0 + 8] = make_float2(m[1], l[1]);
   }
   __syncthreads();
-  const size_t unit = (size_t)bk * a.tiles + tile;
-  for (int i = tid; i < ROWS * D; i += THREADS) {
-    const int r = i / D, c = i % D;
-    const int row = tile * ROWS + r;
-    if (row >= a.rows) break;
-    float mm = -INFINITY, ll = 0.f, v = 0.f;
+  const bool cluster_join = a.splits > 1 && a.splits <= CLUSTER;
+  float* wf = so + WARPS * ROWS * D + 2 * WARPS * ROWS;                 // [WARPS][ROWS] weights of the join
+  float2* js = reinterpret_cast<float2*>(wf + WARPS * ROWS);          // [ROWS] the block's statistics
+  float* jo = reinterpret_cast<float*>(js + ROWS);                      // [ROWS][D] its O, for its cluster
+  const size_t part = ((size_t)bk * a.tiles + tile) * a.splits + split;
+  // output row r of the tile
+  auto out_row = [&](int r, int& h, int& n) {
+    const int row = tile * ROWS + r, g = row / p.Nq;
+    n = row - g * p.Nq;
+    h = hk * p.G + g;
+  };
+  auto write_lse = [&](int r, float m_, float l_) {
+    int h, n;
+    out_row(r, h, n);
+    if (p.lse != nullptr)
+      p.lse[((size_t)b * p.Hq + h) * p.Nq + n] = l_ > 0.f ? (m_ + log2f(l_)) * 0.6931471805599453f : -INFINITY;
+  };
+  if (tid < live) {
+    float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, ss[w * ROWS + r].x);
+    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, ss[w * ROWS + tid].x);
+    float f[WARPS];
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      const float f = mm == -INFINITY ? 0.f : exp2f(ss[w * ROWS + r].x - mm);
-      ll += f * ss[w * ROWS + r].y;
-      v += f * so[(w * ROWS + r) * D + c];
+      f[w] = mm == -INFINITY ? 0.f : exp2f(ss[w * ROWS + tid].x - mm);
+      ll += f[w] * ss[w * ROWS + tid].y;
     }
-    if (a.splits > 1) {
-      a.part[((unit * a.splits + split) * ROWS + r) * D + c] = v;
-      if (c == 0) a.stat[(unit * a.splits + split) * ROWS + r] = make_float2(mm, ll);
+    const float norm = a.splits > 1 ? 1.f : (ll > 0.f ? 1.f / ll : 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) wf[w * ROWS + tid] = f[w] * norm;
+    js[tid] = make_float2(mm, ll);
+    if (a.splits > CLUSTER) a.stat[part * ROWS + tid] = make_float2(mm, ll);
+    if (a.splits == 1) write_lse(tid, mm, ll);
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < live * D; i += THREADS) {
+    const int r = i / D, c = i % D;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += wf[w * ROWS + r] * so[(w * ROWS + r) * D + c];
+    if (cluster_join) {
+      jo[i] = v;
+    } else if (a.splits > 1) {
+      a.part[part * ROWS * D + i] = v;
     } else {
-      const int g = row / p.Nq, n = row % p.Nq, h = hk * p.G + g;
-      put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll > 0.f ? v / ll : 0.f);
-      if (c == 0 && p.lse != nullptr)
-        p.lse[((size_t)b * p.Hq + h) * p.Nq + n] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+      int h, n;
+      out_row(r, h, n);
+      put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), v);
     }
+  }
+  if (cluster_join) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();       // (1, splits, 1): rank = split
+    cluster.sync();
+    for (int i = split * THREADS + tid; i < live * D; i += a.splits * THREADS) {
+      const int r = i / D, c = i % D;
+      float2 st[CLUSTER];
+      float x[CLUSTER], mm = -INFINITY, ll = 0.f, v = 0.f;
+#pragma unroll
+      for (int k = 0; k < CLUSTER; ++k) {                 // all on their way at once
+        st[k] = k < a.splits ? *cluster.map_shared_rank(js + r, k) : make_float2(-INFINITY, 0.f);
+        x[k] = k < a.splits ? *cluster.map_shared_rank(jo + i, k) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < CLUSTER; ++k) mm = fmaxf(mm, st[k].x);
+#pragma unroll
+      for (int k = 0; k < CLUSTER; ++k) {
+        const float f = st[k].x == -INFINITY ? 0.f : exp2f(st[k].x - mm);
+        ll += f * st[k].y;
+        v += f * x[k];
+      }
+      int h, n;
+      out_row(r, h, n);
+      put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll > 0.f ? v / ll : 0.f);
+      if (c == 0) write_lse(r, mm, ll);
+    }
+    cluster.sync();                                       // no block leaves while another reads its shared memory
   }
 }
 
@@ -292,11 +354,22 @@ static Args plan(const Problem& p, void* ws) {
   a.rows = p.G * p.Nq;
   a.tiles = (a.rows + ROWS - 1) / ROWS;
   const int64_t units = (int64_t)a.tiles * p.B * p.Hkv;
-  // split the keys until every SM has a block (a block fills an SM's shared memory)
+  // split the keys until every SM has a block (its rings fill an SM's shared
+  // memory); or, where that many clusters of blocks fit at two an SM, down to one step
+  // a warp, which needs no ring (one token over 512 keys, 64 heads: 4 blocks a head)
   const int64_t most = (p.Nk + MIN_KEYS - 1) / MIN_KEYS;
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(most, SM_COUNT / units));
+  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(most, SM_COUNT / units));
+  a.stages = STAGES;
+  if (most <= CLUSTER && units * most <= 2 * SM_COUNT) {
+    splits = most;
+  } else if (splits > 2 && splits <= CLUSTER) {
+    // clusters of three or five leave SMs of a GPC empty and then wait for a second round
+    splits = splits == CLUSTER ? CLUSTER : splits >= 4 ? 4 : 2;
+    if (splits > 2 && units * splits > 128) splits /= 2;
+  }
   a.per_split = (int)(((p.Nk + splits - 1) / splits + MIN_KEYS - 1) / MIN_KEYS * MIN_KEYS);
   a.splits = (p.Nk + a.per_split - 1) / a.per_split;
+  if (a.per_split == MIN_KEYS) a.stages = 1;
   a.part = static_cast<float*>(ws);
   a.stat = reinterpret_cast<float2*>(a.part + units * a.splits * ROWS * p.d);
   return a;
@@ -305,10 +378,22 @@ static Args plan(const Problem& p, void* ws) {
 template <int D, bool H>
 static cudaError_t run(const Args& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_shared(kernel<D, H>, Lay<D>::SMEM, &done);
+  const cudaError_t e = allow_shared(kernel<D, H>, Lay<D>::smem(STAGES), &done);
   if (e != cudaSuccess) return e;
-  kernel<D, H><<<dim3(a.tiles, a.splits, a.p.B * a.p.Hkv), THREADS, Lay<D>::SMEM, s>>>(a);
-  if (a.splits > 1) join_kernel<D, H><<<dim3(a.rows, a.p.B * a.p.Hkv), D, 0, s>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.tiles, a.splits, a.p.B * a.p.Hkv);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Lay<D>::smem(a.stages);
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
+  attr.val.clusterDim.y = a.splits;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.splits > 1 && a.splits <= CLUSTER ? 1 : 0;
+  const cudaError_t l = cudaLaunchKernelEx(&cfg, kernel<D, H>, a);
+  if (l != cudaSuccess) return l;
+  if (a.splits > CLUSTER) join_kernel<D, H><<<dim3(a.rows, a.p.B * a.p.Hkv), D, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -316,7 +401,7 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
 
 size_t few_workspace(const Problem& p) {
   const few::Args a = few::plan(p, nullptr);
-  return a.splits > 1 ? (size_t)a.tiles * p.B * p.Hkv * a.splits * few::ROWS * (p.d * sizeof(float) + sizeof(float2)) : 0;
+  return a.splits > few::CLUSTER ? (size_t)a.tiles * p.B * p.Hkv * a.splits * few::ROWS * (p.d * sizeof(float) + sizeof(float2)) : 0;
 }
 
 cudaError_t launch_few(const Problem& p, void* ws, cudaStream_t s) {

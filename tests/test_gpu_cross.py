@@ -58,6 +58,9 @@ CASES = [
     (1, 6, 1, 3, 1000, 128, "bf16", "lengths mask"),
     (4, 16, 16, 1, 512, 128, "bf16", "lengths"),
     (1, 2, 1, 17, 4097, 64, "bf16", "none"),
+    (1, 1, 1, 1, 40000, 128, "bf16", "lengths mask"),
+    (5, 6, 6, 2, 1500, 64, "bf16", "lengths"),
+    (1, 30, 30, 1, 700, 128, "fp16", "mask"),
     (2, 3, 3, 129, 65, 128, "bf16", "mask"),
     (2, 4, 2, 200, 64, 64, "fp16", "none"),
     (1, 5, 5, 255, 127, 128, "fp16", "lengths"),
