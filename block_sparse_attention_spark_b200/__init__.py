@@ -16,6 +16,7 @@ __all__ = ["SparkError", "Params", "lib", "params", "num_selected", "workspace_s
            "positional_perm", "select", "attn_fwd", "attn_fwd_joint", "forward", "forward_joint",
            "forward_host", "get_status", "selftest_wait", "RotaryParams", "rotary_params",
            "rotary_validate", "rotary_workspace_size", "alloc_rotary_workspace", "rotary", "rotary_bwd",
+           "forward_rotary", "forward_rotary_workspace_size",
            "CrossParams", "cross_params", "cross_validate", "cross_workspace_size",
            "alloc_cross_workspace", "cross_attn", "cross_attn_bwd",
            "LAYOUTS", "SUMMARIES", "TAILS", "WS", "DTYPES", "PAIRINGS", "SPECTRA"]
@@ -120,6 +121,8 @@ _SIGS = {
     "spark_rotary_workspace_size": (_sz, [_RP]),
     "spark_rotary": (_i32, [_RP, _V, _V, _vp, _vp, _vp, _V, _V, _vp]),
     "spark_rotary_bwd": (_i32, [_RP, _V, _V, _V, _V, _vp, _vp, _vp, _V, _V, _vp, _vp, _vp, _sz, _vp]),
+    "spark_forward_rotary_workspace_size": (_sz, [_P]),
+    "spark_forward_rotary": (_i32, [_P, _RP, _V, _V, _V, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "spark_cross_validate": (_i32, [_CP]),
     "spark_cross_workspace_size": (_sz, [_CP, _i32]),
     "spark_cross_attn": (_i32, [_CP, _V, _V, _V, _vp, _vp, _V, _vp, _vp, _sz, _vp]),
@@ -546,6 +549,26 @@ def rotary_bwd(p: RotaryParams, dq_out, dk_out=None, q=None, k=None, positions=N
     _call(lib().spark_rotary_bwd, "spark_rotary_bwd", dev, p, gq, gk, vq, vk, pos, wq, wk, odq, odk, _ptr(dwq),
           _ptr(dwk), _ptr(ws), 0 if ws is None else ws.numel())
     return dq, dk, dwq, dwk
+
+
+def forward_rotary_workspace_size(p: Params) -> int:
+    return lib().spark_forward_rotary_workspace_size(ctypes.byref(p))
+
+
+def forward_rotary(p: Params, r: RotaryParams, q, k, v, positions=None, q_weight=None, k_weight=None, ws=None,
+                   out=None, lse=None):
+    """The whole pass from a layer's projections: rotary(r, q, k, ...) and then
+    forward(p, ...), q, k and v [B,H,N,d] of any layout. Returns out."""
+    torch = _torch()
+    dev, dt, shp = _device(q, "q"), _dtype_of(0), (p.B, p.H, p.N, p.d)
+    views = [_view(t, n, dev, dt, shp) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    pos, wq, wk = _rotary_extras(r, dev, dt, positions, q_weight, k_weight)
+    ws = _scratch(ws, lambda: forward_rotary_workspace_size(p), dev, "forward_rotary")
+    if out is None:
+        out = torch.empty(shp, dtype=dt, device=dev)
+    _call(lib().spark_forward_rotary, "spark_forward_rotary", dev, p, r, *views, pos, wq, wk, _on(out, "out", dev, dt, shp),
+          None if lse is None else _on(lse, "lse", dev, _dtype_of(2), shp[:3]), ws.data_ptr(), ws.numel())
+    return out
 
 
 def cross_params(B, H, Nq, Nk, d, heads_kv=None, dtype="bf16", scale=None) -> CrossParams:

@@ -534,4 +534,49 @@ spark_status spark_rotary_bwd(const spark_rotary_params* p, const spark_view* dq
   return cudaGetLastError() == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
+size_t spark_forward_rotary_workspace_size(const spark_params* p) {
+  const size_t base = spark_workspace_size(p);
+  return base == 0 ? 0 : (base + 255) / 256 * 256 + 3 * (size_t)p->B * p->H * p->N * p->d * 2;
+}
+
+spark_status spark_forward_rotary(const spark_params* p, const spark_rotary_params* r, const spark_view* q,
+                                  const spark_view* k, const spark_view* v, const float* positions,
+                                  const void* q_weight, const void* k_weight, void* out, float* lse, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  const spark_status vp = spark_validate(p);
+  if (vp != SPARK_OK) return vp;
+  const spark_status vr = rotary::validate(r);
+  if (vr != SPARK_OK) return vr;
+  if (r->B != p->B || r->Hq != p->H || r->Hk != p->H || r->N != p->N || r->d != p->d || r->dtype != SPARK_BF16)
+    return SPARK_ERR_INVALID_ARG;
+  if (positions == nullptr && !rotary::grid_fits(r)) return SPARK_ERR_INVALID_ARG;
+  View seen[3];
+  const spark_view* in[3] = {q, k, v};
+  for (int x = 0; x < 3; ++x)
+    if (!make_view(in[x], p->B, p->H, p->N, p->d, 2, false, &seen[x])) return SPARK_ERR_INVALID_ARG;
+  if (out == nullptr || !aligned(out) || !aligned(q_weight) || !aligned(k_weight) || ((uintptr_t)positions & 3u) != 0)
+    return SPARK_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws)) return SPARK_ERR_INVALID_ARG;
+  if (ws_bytes < spark_forward_rotary_workspace_size(p)) return SPARK_ERR_WORKSPACE;
+  const size_t base = (spark_workspace_size(p) + 255) / 256 * 256, bytes = (size_t)p->B * p->H * p->N * p->d * 2;
+  const int64_t head = (int64_t)p->N * p->d;
+  spark_view to[3];
+  for (int x = 0; x < 3; ++x) to[x] = spark_view{static_cast<char*>(ws) + base + x * bytes, p->H * head, head, p->d};
+  spark_status e = spark_rotary(r, q, k, positions, q_weight, k_weight, &to[0], &to[1], stream);
+  if (e != SPARK_OK) return e;
+  const bool contiguous = (p->B == 1 || seen[2].b == p->H * head) && (p->H == 1 || seen[2].h == head) && seen[2].n == p->d;
+  if (!contiguous) {
+    // the same kernel with no rotated values: a change of layout
+    spark_rotary_params copy = *r;
+    copy.Hk = 0;
+    copy.axes = 1;
+    copy.dims[0] = 0;
+    copy.grid[0] = p->N;
+    e = spark_rotary(&copy, v, nullptr, nullptr, nullptr, nullptr, &to[2], nullptr, stream);
+    if (e != SPARK_OK) return e;
+  }
+  return spark_forward(p, to[0].data, to[1].data, contiguous ? v->data : to[2].data, out, lse, nullptr, nullptr, ws,
+                       spark_workspace_size(p), stream);
+}
+
 }  // extern "C"

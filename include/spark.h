@@ -384,6 +384,18 @@ spark_status spark_rotary_bwd(const spark_rotary_params* p, const spark_view* dq
                               float* dk_weight, void* ws, size_t ws_bytes, cudaStream_t stream);
 spark_status spark_rotary_validate(const spark_rotary_params* p);
 
+/* The whole pass (spark_forward) from a layer's projections: q and k of any
+ * layout get their norm and rotary positions (spark_rotary), v its layout, in
+ * ws, then spark_forward runs on them. Equal to those calls bit for bit.
+ *   p, r     : the same B, N and d; r: Hq = Hk = H, SPARK_BF16
+ *   q, k, v  : views [B,H,N,d] (v contiguous: read where it is)
+ *   ws       : spark_forward_rotary_workspace_size() bytes */
+size_t spark_forward_rotary_workspace_size(const spark_params* p);
+spark_status spark_forward_rotary(const spark_params* p, const spark_rotary_params* r, const spark_view* q,
+                                  const spark_view* k, const spark_view* v, const float* positions,
+                                  const void* q_weight, const void* k_weight, void* out, float* lse,
+                                  void* ws, size_t ws_bytes, cudaStream_t stream);
+
 #define SPARK_CROSS_MAX_TOKENS (1 << 22)
 
 typedef struct {
