@@ -3,15 +3,15 @@
 //   D_i = dO_i . O_i,  P = exp(S - lse),  dV = P^T dO,  dS = P (dO V^T - D),
 //   dQ = scale dS K,  dK = scale dS^T Q   (a key head sums over its query heads)
 //
-// Four launches: stat_kernel forms D and lse log2 e of the rows; rows_kernel (dQ)
-// holds a tile of 128 queries and streams the keys; keys_kernel (dK, dV) holds a
-// tile of 128 keys and streams the queries; sum_kernel joins the shares of dK
-// and dV. S and dP are formed twice, seven products of 128x128x128 a tile pair
+// Three launches: stat_kernel forms D and lse log2 e of the rows; main_kernel's
+// first blocks (rows_body, dQ) hold a tile of 128 queries and stream the keys, its
+// others (keys_body, dK and dV) hold a tile of 128 keys and stream the queries;
+// sum_kernel joins the shares of dK and dV. S and dP are formed twice, seven products of 128x128x128 a tile pair
 // where five would do: adding dQ up over key tiles would take float32 atomics
 // (Nk / 128 times Nq d of them, in an order that changes) or one CTA for
 // all the keys.
 //
-// Both kernels: one persistent CTA per SM, eight warps on the elementwise part
+// Both bodies: one persistent CTA per SM, eight warps on the elementwise part
 // (each thread one row of the tile's TMEM lanes and half of its 128 columns),
 // one warp on TMA, one on MMAs. P and dS are rounded to bf16, the operand type
 // of the MMA, in TMEM, where they are the A operand of the second product of
@@ -28,7 +28,8 @@ namespace bwd {
 using namespace tc;
 
 constexpr int TILE = 128, EW_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9, OUT_WARP0 = 12;
-constexpr int KEYS_THREADS = 320, ROWS_THREADS = 512;
+constexpr int THREADS = 512;               // warps past the ones named stay idle
+static_assert(256 * 176 + 256 * 72 <= THREADS * 128, "registers the block owns");
 constexpr int STAGES = 5;
 
 struct Args {
@@ -42,7 +43,7 @@ struct Args {
   int qtiles, ktiles;
   int ksplits, kper, kitems;                 // shares of a key tile's query tiles, tiles per share
   int qsplits, qitems;                       // shares of a query tile's key tiles
-  int q_per;                                 // items of a CTA in a row; 0: every gridDim.x-th
+  int q_per;                                 // items of a CTA in a row; 0: every blocks-th
   int stay;                                  // at most two key tiles: K stays in shared memory
   float scale, sl2;
   float *lse2, *delta;                       // [B * Hq][NqP]
@@ -53,7 +54,7 @@ struct Args {
 // ------------------------------------------------------------------ D and lse
 // 16 lanes (d = 128; 8 for 64) a row, four rows a lane in flight. Rows past Nq get
 // lse = +inf (so P = 0) and D = 0. Bound by HBM: O and dO are read once.
-// grid (NqP / (1024 / LPR), B * Hq). Forming D inside rows_kernel instead (four
+// grid (NqP / (1024 / LPR), B * Hq). Forming D inside rows_body instead (four
 // warps beside its elementwise ones) was slower: their instructions are the
 // scarce thing there.
 template <int D>
@@ -187,9 +188,8 @@ __device__ __forceinline__ void finish(const Block& k) {
 // What stands in the rows of k and v past the kept ones only reaches their
 // own lanes, which are not written.
 template <int D>
-__global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ void keys_body(const Args& a, unsigned char* smem, int block, int blocks) {
   using L = Lay<D>;
-  extern __shared__ __align__(1024) unsigned char smem[];
   enum { FIXED_FULL, FIXED_EMPTY, S_FULL, P_FULL, DP_FULL, DS_FULL, ACC_FULL, ACC_EMPTY, ROW_FULL, ROW_READ = ROW_FULL + 2,
          FULL = ROW_READ + 2, EMPTY = FULL + STAGES, DRAIN = EMPTY + STAGES, NBAR };
   unsigned counts[NBAR];
@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_cons
   };
   auto kept = [&](int it) { return item_len(a.key_len, a.Nk, it / (a.ksplits * a.ktiles * a.Hkv), nullptr, false); };
 
+  if (k.warp < EW_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (k.warp < EW_WARPS) {
     const int half = k.warp >> 2;
     const uint32_t tb = k.tmem + ((uint32_t)((k.warp & 3) * 32) << 16);
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_cons
       __syncwarp();
       if (k.lane == 0) mbar_arrive(bar(i));
     };
-    for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
+    for (int it = block; ok && it < a.kitems; it += blocks) {
       int b, hk, kt, t0;
       const int tiles = item(it, kept(it), b, hk, kt, t0);
       if (tiles == 0) continue;
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_cons
     if (k.lane == 0) {
       uint32_t nf = 0, nk = 0, nr = 0;
       bool ok = true;
-      for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
+      for (int it = block; ok && it < a.kitems; it += blocks) {
         int b, hk, kt, t0;
         const int tiles = item(it, kept(it), b, hk, kt, t0);
         if (tiles == 0) continue;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_cons
       for (uint32_t x = nk > STAGES ? nk - STAGES : 0; x < nk; ++x) mbar_wait(bar(FULL + x % STAGES), (x / STAGES) & 1u, a.status);
       if (!ok) *k.abort_flag = 1;
     }
-  } else {
+  } else if (k.warp == MMA_WARP) {
     uint32_t nk = 0, nt = 0, ni = 0;
     const uint32_t e = elect_one();
     bool ok = true;
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_cons
     };
     auto wait_stage = [&](uint32_t i) { return wait(FULL + i % STAGES, (i / STAGES) & 1u); };
     const uint32_t sK = k.base, sV = k.base + L::BYTES;
-    for (int it = blockIdx.x; ok && it < a.kitems; it += gridDim.x) {
+    for (int it = block; ok && it < a.kitems; it += blocks) {
       int b, hk, kt, t0;
       const int tiles = item(it, __shfl_sync(0xffffffffu, kept(it), 0), b, hk, kt, t0);
       if (tiles == 0) continue;
@@ -404,11 +406,9 @@ __global__ void __launch_bounds__(KEYS_THREADS, 1) keys_kernel(const __grid_cons
 // One TMA warp brings Q and dO (the next dO, which has to wait for its buffer, is
 // asked into L2 meanwhile), one K and V. Four warps write dQ out.
 template <int D, bool STAY>
-__global__ void __launch_bounds__(ROWS_THREADS, 1) rows_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ void rows_body(const Args& a, unsigned char* smem, int block, int blocks) {
   using L = Lay<D>;
-  static_assert(256 * 176 + 256 * 72 <= ROWS_THREADS * 128, "registers the block owns");
   constexpr int ROW_TMA_WARP = 10;
-  extern __shared__ __align__(1024) unsigned char smem[];
   enum { Q_FULL = 0, Q_READ = 3, DS_FULL = 6, DO_FULL = 8, DO_READ, V_FULL, V_READ, S_FULL, S_READ, DP_FULL, DP_READ,
          ACC_FULL, ACC_READ, K_FULL, K_READ = K_FULL + 3, DRAIN = K_READ + 3, NBAR };
   unsigned counts[NBAR];
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) rows_kernel(const __grid_cons
   // K of tile t of all, tile j of its item
   auto k_at = [&](uint32_t t, int j) { return STAY ? (uint32_t)j : t % NK; };
   auto sK = [&](uint32_t i) { return sV + (1u + i) * L::BYTES; };
-  // this CTA's items: every gridDim.x-th, or q_per in a row
-  const int it0 = a.q_per ? blockIdx.x * a.q_per : blockIdx.x, step = a.q_per ? 1 : gridDim.x;
+  // this CTA's items: every blocks-th, or q_per in a row
+  const int it0 = a.q_per ? block * a.q_per : block, step = a.q_per ? 1 : blocks;
   const int end = a.q_per ? min(it0 + a.q_per, a.qitems) : a.qitems;
   // item: query tile qt of (b, h), key tiles [k0, k0 + tiles)
   auto item = [&](int it, int valid, int& b, int& h, int& qt, int& k0) -> int {
@@ -711,6 +711,14 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) rows_kernel(const __grid_cons
   finish(k);
 }
 
+// Blocks of dQ first, then of dK and dV: those begin as the first ones end.
+template <int D, bool STAY>
+__global__ void __launch_bounds__(THREADS, 1) main_kernel(const __grid_constant__ Args a, int row_blocks) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if ((int)blockIdx.x < row_blocks) rows_body<D, STAY>(a, smem, blockIdx.x, row_blocks);
+  else keys_body<D>(a, smem, blockIdx.x - row_blocks, gridDim.x - row_blocks);
+}
+
 // ------------------------------------------------------------------ shares
 // dK and dV: shares of a key added in order, eight values a thread; the lower
 // 128 threads of a block dV, the upper ones dK. grid (keys / (1024 / d), Hkv, B).
@@ -800,14 +808,13 @@ static Plan plan(const Problem& p, Args* a) {
 
 template <int D>
 static cudaError_t run(const Args& a, cudaStream_t s) {
-  const auto rows = a.stay ? rows_kernel<D, true> : rows_kernel<D, false>;
-  static std::atomic<uint64_t> done[3] = {};
-  cudaError_t e = allow_shared(keys_kernel<D>, Lay<D>::SMEM, &done[0]);
-  if (e == cudaSuccess) e = allow_shared(rows, Lay<D>::SMEM, &done[a.stay ? 1 : 2]);
+  const auto main = a.stay ? main_kernel<D, true> : main_kernel<D, false>;
+  static std::atomic<uint64_t> done[2] = {};
+  const cudaError_t e = allow_shared(main, Lay<D>::SMEM, &done[a.stay ? 1 : 0]);
   if (e != cudaSuccess) return e;
+  const int row_blocks = std::min(a.qitems, SM_COUNT);
   stat_kernel<D><<<dim3((a.NqP * (D / 64) + 127) / 128, a.B * a.Hq), 256, 0, s>>>(a);
-  rows<<<std::min(a.qitems, SM_COUNT), ROWS_THREADS, Lay<D>::SMEM, s>>>(a);
-  keys_kernel<D><<<std::min(a.kitems, SM_COUNT), KEYS_THREADS, Lay<D>::SMEM, s>>>(a);
+  main<<<row_blocks + std::min(a.kitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a, row_blocks);
   sum_kernel<D><<<dim3((a.Nk * (D / 64) + 15) / 16, a.Hkv, a.B), 256, 0, s>>>(a);
   if (a.qsplits > 1) sum_rows_kernel<D><<<dim3((a.Nq * (D / 64) + 15) / 16, a.B * a.Hq), 256, 0, s>>>(a);
   return cudaGetLastError();
