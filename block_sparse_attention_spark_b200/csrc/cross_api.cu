@@ -29,9 +29,17 @@ static Problem problem(const spark_cross_params* p) {
   return c;
 }
 
-// At most 32 rows per key head (query heads of the group times tokens): tiles
-// of 16 rows that read K and V once each; more: tiles of 128 rows of a head.
-static bool few_rows(const Problem& c) { return (int64_t)c.G * c.Nq <= 32; }
+// Rows of a key head (query heads of its group times tokens): up to one tile of
+// 16 always by the few-row kernel, which reads K and V once; more as long as
+// all its tiles together read few enough keys (each tile reads them again), else by the tensor-core
+// kernel's tiles of 128 rows of a head. Measured on both sides of the rule, few
+// against many: d = 128, 512 keys, 16 heads: 32 rows 8.7 / 9.5 us, 64 rows 10.1 /
+// 10.0, 128 rows 12.1 / 11.0; 2 key heads of 2048 keys: 64 rows 9.8 / 14.6, 128
+// rows 17.7 / 14.7; d = 64, 16 key heads of 333 keys: 192 rows 7.8 / 11.2, 384 rows 12.5 / 12.6.
+static bool few_rows(const Problem& c) {
+  const int64_t rows = (int64_t)c.G * c.Nq, tiles = (rows + 15) / 16 * c.B * c.Hkv;
+  return rows <= 16 || (tiles <= 2 * SM_COUNT && tiles * c.Nk <= (c.d == 128 ? 24576 : 98304));
+}
 
 // With a key mask the tensor-core kernels get the kept keys packed to the
 // front (the masks of a call are not known here: the size covers both).

@@ -363,9 +363,10 @@ static Args plan(const Problem& p, void* ws) {
   if (most <= CLUSTER && units * most <= 2 * SM_COUNT) {
     splits = most;
   } else if (splits > 2 && splits <= CLUSTER) {
-    // clusters of three or five leave SMs of a GPC empty and then wait for a second round
-    splits = splits == CLUSTER ? CLUSTER : splits >= 4 ? 4 : 2;
-    if (splits > 2 && units * splits > 128) splits /= 2;
+    // clusters of three or five leave SMs of a GPC empty and wait for a second
+    // round, and so do 16 clusters of eight (37 us where a first round takes 15)
+    splits = splits == CLUSTER && units * CLUSTER <= 64 ? CLUSTER : splits >= 4 ? 4 : 2;
+    if (splits == 4 && units * splits > 128) splits = 2;
   }
   a.per_split = (int)(((p.Nk + splits - 1) / splits + MIN_KEYS - 1) / MIN_KEYS * MIN_KEYS);
   a.splits = (p.Nk + a.per_split - 1) / a.per_split;
