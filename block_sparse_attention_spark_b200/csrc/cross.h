@@ -35,26 +35,41 @@ struct Packed {
   size_t bytes, off_k, off_v, off_count, off_place;
 };
 Packed pack_plan(const Problem& p);
-cudaError_t launch_pack(const Problem& p, const Packed& pk, void* ws, cudaStream_t s);
+struct PackArgs {
+  View k, v;
+  const int32_t* key_len;
+  const uint8_t* mask;                   // null: nothing to pack
+  int B, Hkv, Nk, d;
+  char *ko, *vo;
+  int32_t *count, *place;
+  int* status;
+};
+PackArgs pack_args(const Problem& p, const Packed& pk, void* ws);
+cudaError_t launch_pack(const PackArgs& a, cudaStream_t s);
 
-// Gradients (bf16). p.out is the forward's result; p.key_len counts the kept
-// keys at the front of p.k and p.v; place maps the caller's keys to them (null: itself).
+// Gradients (bf16). p.out is the forward's result. With pack.mask the kept keys
+// are packed first, and p.k, p.v and p.key_len are the packed ones.
 struct Gradients {
   View dout, dq, dk, dv;
   const float* lse;
 };
 size_t bwd_workspace(const Problem& p);
-cudaError_t launch_bwd(const Problem& p, const Gradients& g, const int32_t* place, void* ws, cudaStream_t s);
+cudaError_t launch_bwd(const Problem& p, const Gradients& g, const PackArgs& pack, void* ws, cudaStream_t s);
 
 inline size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 #ifdef __CUDACC__
+}  // namespace cross
+}  // namespace spark
+#include "common.cuh"
+namespace spark {
+namespace cross {
 // Length of item b, clamped; `report` says a bad one to the status word.
 __device__ __forceinline__ int item_len(const int32_t* key_len, int Nk, int b, int* status, bool report) {
   if (key_len == nullptr) return Nk;
   const int n = key_len[b];
   if (n >= 0 && n <= Nk) return n;
-  if (report && status) atomicOr(status, 4);
+  if (report) set_status(status, STATUS_BAD_INPUT);
   return n < 0 ? 0 : Nk;
 }
 #endif

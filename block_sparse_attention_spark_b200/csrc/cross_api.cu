@@ -47,16 +47,17 @@ static size_t forward_workspace(const Problem& c) {
   return few_rows(c) ? few_workspace(c) : align_up(many_workspace(c)) + pack_plan(c).bytes;
 }
 
-// The problem on the packed copies of its kept keys.
-static cudaError_t pack(Problem* c, char* at, cudaStream_t stream, const int32_t** place) {
+// What packing a masked problem's keys into ws takes; the problem is then the packed one.
+static PackArgs pack(Problem* c, char* ws) {
   const Packed pk = pack_plan(*c);
-  const cudaError_t e = launch_pack(*c, pk, at, stream);
-  const int64_t head = (int64_t)c->Nk * c->d;
-  c->k = View{at + pk.off_k, c->Hkv * head, head, c->d};
-  c->v = View{at + pk.off_v, c->Hkv * head, head, c->d};
-  c->key_len = reinterpret_cast<const int32_t*>(at + pk.off_count);
-  if (place) *place = reinterpret_cast<const int32_t*>(at + pk.off_place);
-  return e;
+  const PackArgs a = pack_args(*c, pk, ws);
+  if (c->key_mask != nullptr) {
+    const int64_t head = (int64_t)c->Nk * c->d;
+    c->k = View{a.ko, c->Hkv * head, head, c->d};
+    c->v = View{a.vo, c->Hkv * head, head, c->d};
+    c->key_len = a.count;
+  }
+  return a;
 }
 
 }  // namespace cross
@@ -92,9 +93,8 @@ spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, 
   c.lse = lse;
   c.status = device_status();
   if (cross::few_rows(c)) return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
-  if (c.key_mask != nullptr &&
-      cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::many_workspace(c)), stream, nullptr) != cudaSuccess)
-    return SPARK_ERR_CUDA;
+  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::many_workspace(c)));
+  if (packed.mask != nullptr && cross::launch_pack(packed, stream) != cudaSuccess) return SPARK_ERR_CUDA;
   return cross::launch_many(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
@@ -121,11 +121,8 @@ spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view*
   c.key_len = key_len;
   c.key_mask = key_mask;
   c.status = device_status();
-  const int32_t* place = nullptr;
-  if (key_mask != nullptr &&
-      cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::bwd_workspace(c)), stream, &place) != cudaSuccess)
-    return SPARK_ERR_CUDA;
-  return cross::launch_bwd(c, g, place, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::bwd_workspace(c)));
+  return cross::launch_bwd(c, g, packed, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -19,6 +19,7 @@
 // Sums, P before rounding and all statistics are float32.
 //
 // Bounded waits as in the forward kernels.
+#include "cross_pack.cuh"
 #include "cross_tc.cuh"
 
 namespace spark {
@@ -54,15 +55,23 @@ struct Args {
 // ------------------------------------------------------------------ D and lse
 // 16 lanes (d = 128; 8 for 64) a row, four rows a lane in flight. Rows past Nq get
 // lse = +inf (so P = 0) and D = 0. Bound by HBM: O and dO are read once.
-// grid (NqP / (1024 / LPR), B * Hq). Forming D inside rows_body instead (four
+// The blocks past `blocks` pack the kept keys of a masked call, which needs
+// nothing of this and nothing here needs. Forming D inside rows_body instead (four
 // warps beside its elementwise ones) was slower: their instructions are the
 // scarce thing there.
 template <int D>
-__global__ void __launch_bounds__(256) stat_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(256) stat_kernel(const __grid_constant__ Args a, const __grid_constant__ PackArgs pack,
+                                                  int per_head, int blocks) {
   constexpr int LPR = D / 8, ROWS = 256 / LPR;
-  const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq, l = threadIdx.x % LPR;
-  const int n0 = blockIdx.x * (4 * ROWS) + threadIdx.x / LPR;
-  if (a.key_len != nullptr && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) item_len(a.key_len, a.Nk, b, a.status, true);
+  if ((int)blockIdx.x >= blocks) {
+    pack_block(pack, blockIdx.x - blocks);
+    return;
+  }
+  const int bh = blockIdx.x / per_head, part = blockIdx.x % per_head, b = bh / a.Hq, h = bh % a.Hq, l = threadIdx.x % LPR;
+  const int n0 = part * (4 * ROWS) + threadIdx.x / LPR;
+  // (the lengths of a masked call are counts: pack_block has looked at the caller's)
+  if (a.key_len != nullptr && pack.mask == nullptr && part == 0 && h == 0 && threadIdx.x == 0)
+    item_len(a.key_len, a.Nk, b, a.status, true);
   const char* po = a.o.data + 2 * (b * a.o.b + h * a.o.h + 8 * l);
   const char* pd = a.dov.data + 2 * (b * a.dov.b + h * a.dov.h + 8 * l);
   uint4 x[4], y[4];
@@ -87,7 +96,9 @@ __global__ void __launch_bounds__(256) stat_kernel(const __grid_constant__ Args 
     if (l == 0 && n < a.NqP) {
       const size_t at = (size_t)bh * a.NqP + n;
       a.delta[at] = n < a.Nq ? s : 0.f;
-      a.lse2[at] = n < a.Nq ? a.lse[(size_t)bh * a.Nq + n] * 1.4426950408889634f : INFINITY;
+      // a row without weights (lse = -inf) has no gradient either
+      const float lse = n < a.Nq ? a.lse[(size_t)bh * a.Nq + n] : INFINITY;
+      a.lse2[at] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
     }
   }
 }
@@ -807,13 +818,16 @@ static Plan plan(const Problem& p, Args* a) {
 }
 
 template <int D>
-static cudaError_t run(const Args& a, cudaStream_t s) {
+static cudaError_t run(const Args& a, const PackArgs& pack, cudaStream_t s) {
   const auto main = a.stay ? main_kernel<D, true> : main_kernel<D, false>;
   static std::atomic<uint64_t> done[2] = {};
   const cudaError_t e = allow_shared(main, Lay<D>::SMEM, &done[a.stay ? 1 : 0]);
   if (e != cudaSuccess) return e;
   const int row_blocks = std::min(a.qitems, SM_COUNT);
-  stat_kernel<D><<<dim3((a.NqP * (D / 64) + 127) / 128, a.B * a.Hq), 256, 0, s>>>(a);
+  const int per_head = (a.NqP * (D / 64) + 127) / 128;
+  const int64_t stat_blocks = (int64_t)per_head * a.B * a.Hq, all = stat_blocks + pack_blocks(pack);
+  if (all > INT32_MAX) return cudaErrorInvalidValue;
+  stat_kernel<D><<<(unsigned)all, 256, 0, s>>>(a, pack, per_head, (int)stat_blocks);
   main<<<row_blocks + std::min(a.kitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a, row_blocks);
   sum_kernel<D><<<dim3((a.Nk * (D / 64) + 15) / 16, a.Hkv, a.B), 256, 0, s>>>(a);
   if (a.qsplits > 1) sum_rows_kernel<D><<<dim3((a.Nq * (D / 64) + 15) / 16, a.B * a.Hq), 256, 0, s>>>(a);
@@ -827,7 +841,7 @@ size_t bwd_workspace(const Problem& p) {
   return bwd::plan(p, &a).bytes;
 }
 
-cudaError_t launch_bwd(const Problem& p, const Gradients& g, const int32_t* place, void* ws, cudaStream_t s) {
+cudaError_t launch_bwd(const Problem& p, const Gradients& g, const PackArgs& pack, void* ws, cudaStream_t s) {
   bwd::Args a = {};
   const bwd::Plan pl = bwd::plan(p, &a);
   if (!make_tensor_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE) ||
@@ -840,7 +854,7 @@ cudaError_t launch_bwd(const Problem& p, const Gradients& g, const int32_t* plac
   a.o = p.out; a.dov = g.dout; a.dq = g.dq; a.dk = g.dk; a.dv = g.dv;
   a.lse = g.lse;
   a.key_len = p.key_len;
-  a.place = place;
+  a.place = pack.mask ? pack.place : nullptr;
   a.status = p.status;
   a.scale = p.scale;
   a.sl2 = p.scale * 1.4426950408889634f;
@@ -848,7 +862,7 @@ cudaError_t launch_bwd(const Problem& p, const Gradients& g, const int32_t* plac
   a.delta = reinterpret_cast<float*>(w + pl.off_delta);
   a.part = reinterpret_cast<float*>(w + pl.off_part);
   a.qpart = reinterpret_cast<float*>(w + pl.off_qpart);
-  return p.d == 128 ? bwd::run<128>(a, s) : bwd::run<64>(a, s);
+  return p.d == 128 ? bwd::run<128>(a, pack, s) : bwd::run<64>(a, pack, s);
 }
 
 }  // namespace cross
