@@ -781,22 +781,27 @@ struct Plan {
   size_t off_lse, off_delta, off_part, off_qpart, bytes;
 };
 
-static Plan plan(const Problem& p, Args* a) {
+// even: every item keeps all its keys.
+static Plan plan(const Problem& p, bool even, Args* a) {
   a->B = p.B; a->Hq = p.Hq; a->Hkv = p.Hkv; a->G = p.G; a->Nq = p.Nq; a->Nk = p.Nk;
   a->qtiles = (p.Nq + TILE - 1) / TILE;
   a->ktiles = (p.Nk + TILE - 1) / TILE;
   a->NqP = a->qtiles * TILE;
-  // shares of a key tile's queries: the fewest of those that leave the SMs
-  // within 2% of the least time (rounds of items times tiles an item, and about a
-  // tile's time for each item's start, end and its part of the sums)
+  // shares of a key tile's queries: the fewest of those within 2% of the least
+  // time, in tiles: the rounds of items times the tiles of an item and four more (its
+  // 128 KB of sums, written and read again, take about that long); with lengths
+  // that differ, about 0.6 of the work on average and one item for what it is uneven
   const int64_t units = (int64_t)p.B * p.Hkv * a->ktiles;
   const int64_t L = (int64_t)p.G * a->qtiles;
-  auto cost = [&](int64_t s) { return (units * s + SM_COUNT - 1) / SM_COUNT * ((L + s - 1) / s + 1); };
+  auto cost = [&](int64_t s) {
+    const double item = (double)((L + s - 1) / s + 4);
+    return item * (even ? (double)((units * s + SM_COUNT - 1) / SM_COUNT) : 0.6 * units * s / SM_COUNT + 1.0);
+  };
   const int64_t most = std::min<int64_t>(L, std::max<int64_t>(1, 12 * SM_COUNT / std::max<int64_t>(units, 12)));
-  int64_t least = cost(1);
+  double least = cost(1);
   for (int64_t s = 2; s <= most; ++s) least = std::min(least, cost(s));
   int64_t ks = 1;
-  while (cost(ks) * 100 > least * 102) ++ks;
+  while (cost(ks) > least * 1.02) ++ks;
   a->kper = (int)((L + ks - 1) / ks);
   a->ksplits = (int)((L + a->kper - 1) / a->kper);
   a->kitems = (int)(units * a->ksplits);
@@ -805,7 +810,7 @@ static Plan plan(const Problem& p, Args* a) {
   a->qitems = (int)(rows * a->qsplits);
   a->stay = a->ktiles <= 2 && a->qsplits == 1;
   // lengths differ between items: spread them
-  a->q_per = p.key_len == nullptr && p.key_mask == nullptr ? (a->qitems + SM_COUNT - 1) / SM_COUNT : 0;
+  a->q_per = even ? (a->qitems + SM_COUNT - 1) / SM_COUNT : 0;
   Plan pl;
   size_t o = 0;
   auto take = [&](size_t n) { const size_t at = o; o = align_up(o + n); return at; };
@@ -836,14 +841,15 @@ static cudaError_t run(const Args& a, const PackArgs& pack, cudaStream_t s) {
 
 }  // namespace bwd
 
+// The size does not depend on a call's masks: room for either plan.
 size_t bwd_workspace(const Problem& p) {
   bwd::Args a = {};
-  return bwd::plan(p, &a).bytes;
+  return std::max(bwd::plan(p, true, &a).bytes, bwd::plan(p, false, &a).bytes);
 }
 
 cudaError_t launch_bwd(const Problem& p, const Gradients& g, const PackArgs& pack, void* ws, cudaStream_t s) {
   bwd::Args a = {};
-  const bwd::Plan pl = bwd::plan(p, &a);
+  const bwd::Plan pl = bwd::plan(p, p.key_len == nullptr, &a);
   if (!make_tensor_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE) ||
       !make_tensor_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
       !make_tensor_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
