@@ -432,7 +432,7 @@ def _device(t, name):
 def _call(fn, where, dev, *args):
     """A library call on the device's current stream, with that device current."""
     torch = _torch()
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -506,10 +506,12 @@ def rotary(p: RotaryParams, q, k=None, positions=None, q_weight=None, k_weight=N
         raise TypeError("k: given exactly when the parameters have key heads")
     vq = _view(q, "q", dev, dt, qs)
     vk = None if k is None else _view(k, "k", dev, dt, ks)
-    pos, wq, wk = _rotary_extras(p, dev, dt, positions, q_weight, k_weight)
+    pos = wq = wk = None
+    if positions is not None or q_weight is not None or k_weight is not None:
+        pos, wq, wk = _rotary_extras(p, dev, dt, positions, q_weight, k_weight)
     if out is None:
-        qo = q.new_empty(qs)
-        ko = None if k is None else k.new_empty(ks)
+        qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         qo, ko = out
     wqo = _view(qo, "q_out", dev, dt, qs)
@@ -618,7 +620,7 @@ def cross_attn(p: CrossParams, q, k, v, ws=None, key_len=None, key_mask=None, re
     vq, vk, vv = _view(q, "q", dev, dt, qs), _view(k, "k", dev, dt, ks), _view(v, "v", dev, dt, ks)
     kl, km = _cross_masks(p, dev, key_len, key_mask)
     if out is None:
-        out = q.new_empty(qs)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     vo = _view(out, "out", dev, dt, qs)
     lse = q.new_empty(qs[:3], dtype=_dtype_of(2)) if return_lse else None
     ws = _scratch(ws, lambda: cross_workspace_size(p), dev, "cross_attn")

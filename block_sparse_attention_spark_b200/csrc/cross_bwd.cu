@@ -6,10 +6,10 @@
 // Three launches: stat_kernel forms D and lse log2 e of the rows; main_kernel's
 // first blocks (rows_body, dQ) hold a tile of 128 queries and stream the keys, its
 // others (keys_body, dK and dV) hold a tile of 128 keys and stream the queries;
-// sum_kernel joins the shares of dK and dV. S and dP are formed twice, seven products of 128x128x128 a tile pair
-// where five would do: adding dQ up over key tiles would take float32 atomics
-// (Nk / 128 times Nq d of them, in an order that changes) or one CTA for
-// all the keys.
+// sum_kernel joins the shares of dK and dV. S and dP are formed twice, seven
+// products of 128x128x128 a tile pair where five would do: adding dQ up over key
+// tiles would take float32 atomics (Nk / 128 times Nq d of them, in an order
+// that changes) or one CTA for all the keys.
 //
 // Both bodies: one persistent CTA per SM, eight warps on the elementwise part
 // (each thread one row of the tile's TMEM lanes and half of its 128 columns),
@@ -17,6 +17,12 @@
 // of the MMA, in TMEM, where they are the A operand of the second product of
 // each chain. Products have N = 128 throughout (N = 64 runs at half the rate).
 // Sums, P before rounding and all statistics are float32.
+//
+// Measured (72,576 queries of 40 heads over 256 keys, d = 128): 1,520 us (1,713 in
+// a loop of 0.15 s): statistics 241 us = 6.2 TB/s, dQ about 600, dK and dV 620 =
+// 1.23 PFLOP/s of MMA work, 90% of what the card sustains in cuBLAS under its
+// 1,000 W (1.37): power bounds it (SM clock 1.52 GHz), exponentials on the FMA pipe
+// or fewer instructions in the elementwise warps changed nothing.
 //
 // Bounded waits as in the forward kernels.
 #include "cross_pack.cuh"

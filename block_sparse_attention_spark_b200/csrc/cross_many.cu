@@ -4,19 +4,19 @@
 // key head (each tile's rows are tokens of one query head) against all the
 // kept keys of that head, or against one share of them when there are fewer
 // tiles than SMs (the shares are joined by join_kernel). K and V stream in
-// tiles of 128 keys through one ring of five 32 KB stages that both row tiles
-// read, which halves the L2 traffic of one tile alone (at 72,576 queries by
-// 512 keys one row tile per CTA would ask 13 TB/s of it).
+// tiles of 128 keys through one ring (four 32 KB stages at d = 128) that both
+// row tiles read, which halves the L2 traffic of one tile alone (at 72,576
+// queries by 512 keys one row tile per CTA would ask 13 TB/s of it).
 //
 // TMEM (512 columns): S of the two tiles at 0 and 128, O at 256 and 384; P
-// (16 bits, two keys a column) overwrites the first half of its S. One thread
+// (16 bits, two keys a column) overwrites the first half of its S. One warp
 // issues, in turn for the two tiles, P_j V_j and then S_{j+1} = Q K_{j+1}^T:
 // while the tensor cores work for one tile, the other tile's four warps (one
-// thread per row) turn S into P. MMAs of one thread complete in issue order,
-// so S_{j+1} arriving says that P_j V_j is done: O may be rescaled, the next
-// tile's first S may overwrite P, without further barriers. The next item's Q
-// and K are loaded while this one's last tiles run, and its first S is issued before
-// the row tile's O has been written out.
+// thread per row) turn S into P and hand it over in two halves of 64 keys. MMAs
+// of one thread complete in issue order, so S_{j+1} arriving says that P_j V_j
+// is done: O may be rescaled, the next tile's first S may overwrite P, without
+// further barriers. Four more warps write O out while the softmax is at the
+// next item, whose Q (a third buffer) and K are already there.
 //
 // The softmax is online with a lazy reference: the row's reference maximum
 // moves (and O is rescaled in TMEM) only when a logit passes it by 2^8. Sums
@@ -24,6 +24,14 @@
 // of the MMA. The last tile of an item runs with N (and for P V, K) cut to the
 // next multiple of 16 of its keys; V rows between are zeroed in shared memory,
 // whatever they hold, because 0 * NaN is NaN.
+//
+// Measured (bf16, d = 128): 9,472 queries of 8 heads over 2,048 keys 71 us =
+// 1,120 TFLOP/s; 72,576 queries of 40 heads over 512 keys 727 us = 1,046 (850 us
+// in a loop of 0.15 s); over 77 keys 331 us = 4.5 TB/s. What bounds it: the chain
+// S -> P -> P V of a row tile (about 2,100 clocks of softmax and 1,000 to 1,300 of
+// MMAs and hand-overs a tile, the other row tile beside it), and the 1,000 W power cap: the SMs
+// run at 1.56 GHz under it. Leaving out every exponential gained 2%, so the
+// exponentials are not worth moving to the FMA pipe (tried: 2 to 13% slower).
 //
 // Every wait is bounded (2 s): on expiry the status word is set, copies and
 // MMAs in flight are waited for (bounded again), TMEM is freed, the kernel returns.

@@ -321,8 +321,12 @@ size_t spark_workspace_region(const spark_params* p, int32_t region, size_t* byt
  * (the token stride at least d when there is more than one token; batch and
  * head strides of a read tensor may be 0, a shared row); a written view
  * must not overlap itself. Strides of axes of extent 1 are not looked at. All
- * pointers are on the current device. d is 64 or 128. Everything else is as
- * for the calls above: asynchronous on the stream, no allocation, no fallback.
+ * pointers are on the current device. An output overlaps no input unless the call
+ * says so. d is 64 or 128. Everything else is as for the calls above: asynchronous
+ * on the stream, no allocation, no fallback, and calls whose kernels may overlap
+ * (other streams, graphs replayed at the same time) need a workspace each.
+ * Inputs are finite except where a call says that they are not looked at.
+ * Make the first call on a device outside of a stream capture.
  * Sizes below 1 are SPARK_ERR_INVALID_ARG (masks may still leave no key). */
 typedef struct {
   const void* data;
@@ -418,7 +422,8 @@ typedef struct {
  *   lse          : [B,Hq,Nq] float32 device or NULL
  *   ws           : workspace of spark_cross_workspace_size(p, 0) bytes (scratch;
  *                  calls that may overlap need one each)
- * P is rounded to the tensors' type for P V, sums and statistics are float32. */
+ * P is rounded to the tensors' type for P V, sums and statistics are float32.
+ * One launch, two with a mask or where the keys are split over blocks. */
 size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd);
 spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, const spark_view* k,
                               const spark_view* v, const int32_t* key_len, const uint8_t* key_mask,
@@ -428,7 +433,7 @@ spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, 
 /* Its gradient: dq, dk, dv from the gradient dout of out, with out and lse as
  * spark_cross_attn gave them. Rows of dk and dv that are not kept are zero; a
  * shared key head gets the sum over its query heads. Equal calls give equal
- * bits (no atomics). bf16 only: the products P (dO V^T - D) of small
+ * bits (no atomics). A row whose lse is -inf has no gradient. bf16 only: the products P (dO V^T - D) of small
  * gradients fall below fp16's normal range (SPARK_ERR_UNSUPPORTED).
  *   ws : workspace of spark_cross_workspace_size(p, 1) bytes */
 spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view* q, const spark_view* k,
