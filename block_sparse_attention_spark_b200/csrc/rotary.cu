@@ -24,6 +24,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "views.h"
 
@@ -59,63 +61,111 @@ struct Args {
 // 2j, 2j+1 of the register array
 enum { CONTIG = 0, SPLIT4 = 1, SINGLES = 2 };
 
+// Two 16-bit values of a word.
 template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ void unpack(uint32_t w, float& lo, float& hi) {
+  if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+    lo = bf_lo(w);
+    hi = bf_hi(w);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x;
+    hi = f.y;
+  }
+}
 template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ float from_f(float v) { return v; }
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  uint32_t w;
+  if constexpr (std::is_same<T, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Pack {
-  T v[N];
-};
-
-// A lane's eight values of a row (raw, converted on use).
+// A lane's eight values of a row as they come: four words of two (16-bit types)
+// or eight. Value order: pair j of the lane is values 2j, 2j+1 of get and put;
+// with SPLIT4 the first half of the words holds the pairs' first values.
 template <typename T, int MODE>
 struct Row {
-  T v[8];
+  static constexpr int WORDS = 2 * sizeof(T);          // 4 or 8
+  uint32_t w[WORDS];
+  __device__ __forceinline__ static const T* first(const T* row, int l, int npairs) {
+    return row + (MODE == SPLIT4 && 4 * l < npairs ? 4 * l : 8 * l);
+  }
+  __device__ __forceinline__ static const T* second(const T* row, int l, int npairs) {
+    return row + (MODE == SPLIT4 && 4 * l < npairs ? npairs + 4 * l : 8 * l + 4);
+  }
   __device__ __forceinline__ void load(const T* row, int l, int npairs) {
-    if constexpr (MODE == CONTIG) {
-      *reinterpret_cast<Pack<T, 8>*>(v) = *reinterpret_cast<const Pack<T, 8>*>(row + 8 * l);
-    } else if constexpr (MODE == SPLIT4) {
-      // the lanes before R / 8 hold four pairs, the others eight kept values
-      const bool pairs = 4 * l < npairs;
-      const Pack<T, 4> a = *reinterpret_cast<const Pack<T, 4>*>(row + (pairs ? 4 * l : 8 * l));
-      const Pack<T, 4> b = *reinterpret_cast<const Pack<T, 4>*>(row + (pairs ? npairs + 4 * l : 8 * l + 4));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) { v[2 * j] = a.v[j]; v[2 * j + 1] = b.v[j]; }
-    } else {
+    if constexpr (MODE == SINGLES) {
+      T v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = row[at(l, j, npairs)];
+#pragma unroll
+      for (int j = 0; j < WORDS; ++j) w[j] = reinterpret_cast<const uint32_t*>(v)[j];
+    } else if constexpr (MODE == CONTIG) {
+#pragma unroll
+      for (int j = 0; j < WORDS; j += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(row + 8 * l) + j);
+        w[j] = x.x; w[j + 1] = x.y; w[j + 2] = x.z; w[j + 3] = x.w;
+      }
+    } else if constexpr (WORDS == 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(first(row, l, npairs));
+      const uint2 y = *reinterpret_cast<const uint2*>(second(row, l, npairs));
+      w[0] = x.x; w[1] = x.y; w[2] = y.x; w[3] = y.y;
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4*>(first(row, l, npairs));
+      const uint4 y = *reinterpret_cast<const uint4*>(second(row, l, npairs));
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+      w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
     }
   }
   __device__ __forceinline__ void store(T* row, int l, int npairs) const {
-    if constexpr (MODE == CONTIG) {
-      *reinterpret_cast<Pack<T, 8>*>(row + 8 * l) = *reinterpret_cast<const Pack<T, 8>*>(v);
-    } else if constexpr (MODE == SPLIT4) {
-      const bool pairs = 4 * l < npairs;
-      Pack<T, 4> a, b;
+    if constexpr (MODE == SINGLES) {
+      T v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) { a.v[j] = v[2 * j]; b.v[j] = v[2 * j + 1]; }
-      *reinterpret_cast<Pack<T, 4>*>(row + (pairs ? 4 * l : 8 * l)) = a;
-      *reinterpret_cast<Pack<T, 4>*>(row + (pairs ? npairs + 4 * l : 8 * l + 4)) = b;
-    } else {
+      for (int j = 0; j < WORDS; ++j) reinterpret_cast<uint32_t*>(v)[j] = w[j];
 #pragma unroll
       for (int j = 0; j < 8; ++j) row[at(l, j, npairs)] = v[j];
+    } else if constexpr (MODE == CONTIG) {
+#pragma unroll
+      for (int j = 0; j < WORDS; j += 4)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(row + 8 * l) + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+    } else if constexpr (WORDS == 4) {
+      *reinterpret_cast<uint2*>(const_cast<T*>(first(row, l, npairs))) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(const_cast<T*>(second(row, l, npairs))) = make_uint2(w[2], w[3]);
+    } else {
+      *reinterpret_cast<uint4*>(const_cast<T*>(first(row, l, npairs))) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(const_cast<T*>(second(row, l, npairs))) = make_uint4(w[4], w[5], w[6], w[7]);
     }
   }
-  // index in the row of register value j
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (WORDS == 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[MODE == SPLIT4 ? 2 * (j & 3) + (j >> 2) : j] = __uint_as_float(w[j]);
+    } else if constexpr (MODE == SPLIT4) {
+      unpack<T>(w[0], f[0], f[2]);
+      unpack<T>(w[1], f[4], f[6]);
+      unpack<T>(w[2], f[1], f[3]);
+      unpack<T>(w[3], f[5], f[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unpack<T>(w[j], f[2 * j], f[2 * j + 1]);
+    }
+  }
+  __device__ __forceinline__ void put(const float* f) {
+    if constexpr (WORDS == 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[MODE == SPLIT4 ? 2 * (j & 3) + (j >> 2) : j]);
+    } else if constexpr (MODE == SPLIT4) {
+      w[0] = pack<T>(f[0], f[2]);
+      w[1] = pack<T>(f[4], f[6]);
+      w[2] = pack<T>(f[1], f[3]);
+      w[3] = pack<T>(f[5], f[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack<T>(f[2 * j], f[2 * j + 1]);
+    }
+  }
+  // index in the row of value j
   __device__ __forceinline__ static int at(int l, int j, int npairs) {
     if constexpr (MODE == CONTIG) return 8 * l + j;
     if constexpr (MODE == SPLIT4)
@@ -159,8 +209,7 @@ template <typename T, int D, int MODE, bool NORM>
 __device__ __forceinline__ void forward_row(Row<T, MODE>& x, const float* c, const float* s, const float* w,
                                             unsigned live, float eps) {
   float f[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = to_f(x.v[j]);
+  x.get(f);
   if constexpr (NORM) {
     float ss = 0.f;
 #pragma unroll
@@ -170,8 +219,7 @@ __device__ __forceinline__ void forward_row(Row<T, MODE>& x, const float* c, con
     for (int j = 0; j < 8; ++j) f[j] *= r * w[j];
   }
   turn<1>(f, c, s, live);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x.v[j] = from_f<T>(f[j]);
+  x.put(f);
 }
 
 // y: gradient of the row's result, becomes the gradient of the row x.
@@ -179,29 +227,27 @@ template <typename T, int D, int MODE, bool NORM>
 __device__ __forceinline__ void backward_row(Row<T, MODE>& y, const Row<T, MODE>& x, const float* c, const float* s,
                                              const float* w, unsigned live, float eps, bool active, float* dw) {
   float f[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = to_f(y.v[j]);
+  y.get(f);
   turn<-1>(f, c, s, live);
   if constexpr (NORM) {
     float xs[8], ss = 0.f, xg = 0.f;
+    x.get(xs);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      xs[j] = to_f(x.v[j]);
       ss = fmaf(xs[j], xs[j], ss);
       xg = fmaf(xs[j], f[j] * w[j], xg);
     }
     ss = row_sum<D / 8>(ss);
     xg = row_sum<D / 8>(xg);
     const float r = rsqrtf(ss * (1.f / D) + eps);
-    const float t = r * r * xg * (1.f / D);
+    const float t = r * r * xg * (1.f / D), mine = active ? r : 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (active) dw[j] = fmaf(f[j], xs[j] * r, dw[j]);
-      f[j] = r * (f[j] * w[j] - xs[j] * t);
+      dw[j] = fmaf(f[j], xs[j] * mine, dw[j]);
+      f[j] = fmaf(r * w[j], f[j], -(xs[j] * (r * t)));
     }
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y.v[j] = from_f<T>(f[j]);
+  y.put(f);
 }
 
 // The heads [h0, h1) of a tensor at one token.
@@ -213,8 +259,7 @@ __device__ __forceinline__ void heads(const Tensor& t, int b, int n, int h0, int
   if constexpr (NORM) {
     Row<T, MODE> wr;
     wr.load(static_cast<const T*>(t.weight), l, npairs);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = to_f(wr.v[j]);
+    wr.get(w);
   }
   const T* pi = reinterpret_cast<const T*>(t.in.data) + b * t.in.b + n * t.in.n;
   const T* px = BWD && NORM ? reinterpret_cast<const T*>(t.x.data) + b * t.x.b + n * t.x.n : nullptr;
