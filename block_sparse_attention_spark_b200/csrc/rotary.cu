@@ -10,17 +10,19 @@
 // thread owns eight values (four pairs) of one token's row, forms their four
 // cosines and sines once (turns in 64 bits: position times frequency, reduced
 // to [-1/2, 1/2], then 32-bit sincospi), and walks heads of q or of k with
-// them in registers, four rows (gradient: two) in flight. A warp's 32 lanes hold
+// them in registers, four rows (some gradients: two) in flight. A warp's 32 lanes hold
 // two (d = 128) or four (d = 64) rows, so the mean of squares is a shuffle over
 // 16 or 8 lanes. A block holds 256 / (d / 8) tokens of one tensor; heads are
 // split over blocks when tokens alone do not fill the GPU.
 //
 // What counts is how many warps are resident: the forward kernel held to 64
 // registers (four blocks an SM) reads and writes 72,576 tokens of 80 heads
-// (bf16, d = 128) in 463 us = 6.4 TB/s, with 80 registers in 510; a software
+// (bf16, d = 128) in 461 us = 6.4 TB/s, with 80 registers in 510; a software
 // pipeline of the loads (more in flight a thread, fewer warps) took 508 to 750.
 // Heads a block: for at least six blocks an SM in all (24: the angles are
-// formed for four heads at a time, 41 against 32 us at 7,110 tokens of 32 heads).
+// formed for four heads at a time, 41 against 32 us at 7,110 tokens of 32 heads;
+// the gradient's blocks with partial sums, 888: 87 us, 444: 88, 2,664: 90).
+// 16-bit values are converted in pairs: value by value those took 31 us, now 29.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -33,7 +35,7 @@ namespace spark {
 namespace rotary {
 
 constexpr int THREADS = 256;
-constexpr int UNROLL_F = 4, UNROLL_B = 2;  // rows in flight per thread
+constexpr int ROWS = 4;                    // rows in flight per thread (heads are shared out in fours)
 constexpr int BWD_BLOCKS = SM_COUNT * 6;   // blocks of the gradient where it has partial sums of dw
 
 struct Tensor {
@@ -254,7 +256,10 @@ __device__ __forceinline__ void backward_row(Row<T, MODE>& y, const Row<T, MODE>
 template <typename T, int D, int MODE, bool BWD, bool NORM>
 __device__ __forceinline__ void heads(const Tensor& t, int b, int n, int h0, int h1, int l, int npairs, float eps,
                                       const float* c, const float* s, unsigned live, bool active, float* dw) {
-  constexpr int UNROLL = BWD ? UNROLL_B : UNROLL_F;
+  // gradient: two rows of 32-bit values, or of scattered ones, fill the registers;
+  // with four of 16 bits instead of two 87 against 91 us (16 heads of 32,256,
+  // norm) and 227 against 250 (80 heads of 36,288, none: 6.5 TB/s)
+  constexpr int UNROLL = BWD && (sizeof(T) == 4 || MODE == SINGLES) ? 2 : ROWS;
   float w[8];
   if constexpr (NORM) {
     Row<T, MODE> wr;
@@ -290,8 +295,8 @@ __device__ __forceinline__ void heads(const Tensor& t, int b, int n, int h0, int
 }
 
 // NORMED: some tensor has a weight. Blocks an SM: the gradient without a norm at
-// four (64 registers; 40 + 40 heads of 36,288 tokens 254 us, at three 286), with
-// one at three (at four it spills: 117 against 94 us for 16 heads of 32,256).
+// four (64 registers), with one at three (at four some forms spill: 98 against
+// 91 us for 16 heads of 32,256 in bf16, 167 against 143 for 36,288 in fp32).
 template <typename T, int D, int MODE, bool BWD, bool NORMED>
 __global__ void __launch_bounds__(THREADS, BWD && NORMED ? 3 : 4) kernel(const __grid_constant__ Args a) {
   constexpr int LPR = D / 8, TOK = THREADS / LPR;
@@ -428,7 +433,7 @@ static bool grid_fits(const spark_rotary_params* p) {
 }
 
 // Frequencies and the split of the work; the pointers are filled in by the calls.
-static Args plan(const spark_rotary_params* p, const float* pos, bool bwd) {
+static Args plan(const spark_rotary_params* p, const float* pos) {
   Args a = {};
   a.N = p->N;
   a.axes = p->axes;
@@ -453,7 +458,7 @@ static Args plan(const spark_rotary_params* p, const float* pos, bool bwd) {
   }
   // heads per block: they share a token's angles, so as many as still give every
   // SM a few blocks
-  const int tok = THREADS / (p->d / 8), unroll = bwd ? UNROLL_B : UNROLL_F;
+  const int tok = THREADS / (p->d / 8);
   a.tiles = (p->N + tok - 1) / tok;
   const int64_t tiles = (int64_t)a.tiles * p->B, want = SM_COUNT * 6;
   const int heads = p->Hq + p->Hk;
@@ -462,7 +467,7 @@ static Args plan(const spark_rotary_params* p, const float* pos, bool bwd) {
     Tensor& t = a.t[x];
     t.H = x ? p->Hk : p->Hq;
     if (t.H == 0) continue;
-    t.per_split = (int)std::min<int64_t>(t.H, (share + unroll - 1) / unroll * unroll);
+    t.per_split = (int)std::min<int64_t>(t.H, (share + ROWS - 1) / ROWS * ROWS);
     t.splits = (t.H + t.per_split - 1) / t.per_split;
     t.per_split = (t.H + t.splits - 1) / t.splits;
     t.items = (int)std::min<int64_t>(tiles * t.splits, INT32_MAX);
@@ -513,7 +518,7 @@ spark_status spark_rotary(const spark_rotary_params* p, const spark_view* q, con
   const spark_status v = rotary::validate(p);
   if (v != SPARK_OK) return v;
   if (positions == nullptr && !rotary::grid_fits(p)) return SPARK_ERR_INVALID_ARG;
-  rotary::Args a = rotary::plan(p, positions, false);
+  rotary::Args a = rotary::plan(p, positions);
   const int es = rotary::elem(p);
   if (!make_view(q, p->B, p->Hq, p->N, p->d, es, false, &a.t[0].in) ||
       !make_view(q_out, p->B, p->Hq, p->N, p->d, es, true, &a.t[0].out))
@@ -538,7 +543,7 @@ spark_status spark_rotary_bwd(const spark_rotary_params* p, const spark_view* dq
   const spark_status v = rotary::validate(p);
   if (v != SPARK_OK) return v;
   if (positions == nullptr && !rotary::grid_fits(p)) return SPARK_ERR_INVALID_ARG;
-  rotary::Args a = rotary::plan(p, positions, true);
+  rotary::Args a = rotary::plan(p, positions);
   const int es = rotary::elem(p);
   const spark_view* views[2][3] = {{dq_out, q, dq}, {dk_out, k, dk}};
   const void* weights[2] = {q_weight, p->Hk > 0 ? k_weight : nullptr};
