@@ -198,11 +198,13 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
         o[n][2 * r + 1] *= c;
       }
     }
+    // (logits all -inf so far: exp2(-inf - 0) = 0; NaN stays NaN and reaches sum and O)
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
     for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[n][e] = m[e >> 1] == -INFINITY ? 0.f : exp2f(s[n][e] - m[e >> 1]);
+        s[n][e] = exp2f(s[n][e] - ref[e >> 1]);
         l[e >> 1] += s[n][e];
       }
 #pragma unroll
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
     int h, n;
     out_row(r, h, n);
     if (p.lse != nullptr)
-      p.lse[((size_t)b * p.Hq + h) * p.Nq + n] = l_ > 0.f ? (m_ + log2f(l_)) * 0.6931471805599453f : -INFINITY;
+      p.lse[((size_t)b * p.Hq + h) * p.Nq + n] = l_ == 0.f ? -INFINITY : (m_ + log2f(l_)) * 0.6931471805599453f;
   };
   if (tid < live) {
     float mm = -INFINITY, ll = 0.f;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
       f[w] = mm == -INFINITY ? 0.f : exp2f(ss[w * ROWS + tid].x - mm);
       ll += f[w] * ss[w * ROWS + tid].y;
     }
-    const float norm = a.splits > 1 ? 1.f : (ll > 0.f ? 1.f / ll : 0.f);
+    const float norm = a.splits > 1 ? 1.f : (ll == 0.f ? 0.f : 1.f / ll);
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) wf[w * ROWS + tid] = f[w] * norm;
     js[tid] = make_float2(mm, ll);
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
       }
       int h, n;
       out_row(r, h, n);
-      put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll > 0.f ? v / ll : 0.f);
+      put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll == 0.f ? 0.f : v / ll);
       if (c == 0) write_lse(r, mm, ll);
     }
     cluster.sync();                                       // no block leaves while another reads its shared memory
@@ -335,17 +337,17 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ Args a)
   const int r = row % ROWS;
   float mm = -INFINITY, ll = 0.f, v = 0.f;
   for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.stat[(unit * a.splits + s) * ROWS + r].x);
-  if (mm > -INFINITY)
-    for (int s = 0; s < a.splits; ++s) {
-      const float2 st = a.stat[(unit * a.splits + s) * ROWS + r];
-      const float f = exp2f(st.x - mm);
-      ll += f * st.y;
-      v += f * a.part[((unit * a.splits + s) * ROWS + r) * D + c];
-    }
+  const float ref = mm == -INFINITY ? 0.f : mm;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 st = a.stat[(unit * a.splits + s) * ROWS + r];
+    const float f = exp2f(st.x - ref);
+    ll += f * st.y;
+    v += f * a.part[((unit * a.splits + s) * ROWS + r) * D + c];
+  }
   const int g = row / p.Nq, n = row % p.Nq, h = hk * p.G + g;
-  put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll > 0.f ? v / ll : 0.f);
+  put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll == 0.f ? 0.f : v / ll);
   if (c == 0 && p.lse != nullptr)
-    p.lse[((size_t)b * p.Hq + h) * p.Nq + n] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    p.lse[((size_t)b * p.Hq + h) * p.Nq + n] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
 static Args plan(const Problem& p, void* ws) {

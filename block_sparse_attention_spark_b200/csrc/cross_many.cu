@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         const uint32_t oc = tb + O_COL + 128u * (uint32_t)s;
         const int g = t / a.tokens, n = (t % a.tokens) * ROWS + r, h = w.hk * a.G + g;
         const bool live = n < a.Nq;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         float* part = a.part + ((size_t)it * SLOTS + s) * ROWS * D + (size_t)r * D;
         char* dst = a.out.data + 2 * (w.b * a.out.b + h * a.out.h + (int64_t)n * a.out.n);
 #pragma unroll 1
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         }
         if (live && a.splits > 1) a.stat[((size_t)it * SLOTS + s) * ROWS + r] = make_float2(m, l);
         if (live && a.splits == 1 && a.lse != nullptr)
-          a.lse[((size_t)w.b * a.Hq + h) * a.Nq + n] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          a.lse[((size_t)w.b * a.Hq + h) * a.Nq + n] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       }
     }
     if (!ok) atomicExch(&abort_sh, 1);
@@ -525,24 +525,23 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   float l = 0.f, o[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  if (m > -INFINITY) {
+  const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-      const float2 st = a.stat[row(s)];
-      const float f = exp2f(st.x - m);
-      l += f * st.y;
-      const float* src = a.part + row(s) * D + lane * (D / 32);
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 st = a.stat[row(s)];
+    const float f = exp2f(st.x - ref);
+    l += f * st.y;
+    const float* src = a.part + row(s) * D + lane * (D / 32);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
-    }
+    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   char* dst = a.out.data + 2 * (b * a.out.b + h * a.out.h + (int64_t)n * a.out.n) + lane * (D / 16);
 #pragma unroll
   for (int e = 0; e < D / 64; ++e)
     *reinterpret_cast<uint32_t*>(dst + 4 * e) = pack2<H>(o[2 * e] * inv, o[2 * e + 1] * inv);
   if (lane == 0 && a.lse != nullptr)
-    a.lse[((size_t)b * a.Hq + h) * a.Nq + n] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    a.lse[((size_t)b * a.Hq + h) * a.Nq + n] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 static void plan(const Problem& p, Args* a) {

@@ -174,3 +174,29 @@ def test_cross_attention_on_another_stream_and_in_two_graphs(Nq):
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want) and torch.equal(outs[1], want2)
     assert spark.get_status() == 0
+
+
+# one block a row tile, a cluster of them, shares joined by a second launch; the same of the tensor-core kernel
+@pytest.mark.parametrize("H,Nq,Nk", [(64, 3, 90), (4, 3, 700), (1, 1, 40000), (160, 300, 200), (2, 300, 5000)])
+def test_cross_attention_nan_rows_stay_nan_and_alone(H, Nq, Nk):
+    """A query row of NaN gives a row of NaN, not zeros, and no other row changes."""
+    p, q, k, v, _ = inputs(1, H, H, Nq, Nk, 64)
+    out, lse = spark.cross_attn(p, q, k, v, return_lse=True)
+    q = q.clone()
+    q[:, 0, Nq // 2] = float("nan")
+    got, got_lse = spark.cross_attn(p, q, k, v, return_lse=True)
+    assert got[:, 0, Nq // 2].isnan().all() and got_lse[:, 0, Nq // 2].isnan().all()
+    got[:, 0, Nq // 2], got_lse[:, 0, Nq // 2] = out[:, 0, Nq // 2], lse[:, 0, Nq // 2]
+    assert torch.equal(got, out) and torch.equal(got_lse, lse)
+
+
+def test_cross_attention_mask_of_many_keys():
+    """Masks whose packing takes several pieces a block, with an end inside a piece."""
+    p, q, k, v, kw = inputs(2, 2, 1, 150, 140001, 64, mask="lengths mask")
+    kw["key_len"][0], kw["key_len"][1] = 140001, 130000
+    out, lse = spark.cross_attn(p, q, k, v, return_lse=True, **kw)
+    assert spark.get_status() == 0
+    ref = o64.Cross(q, k, v, **kw)
+    bo, bl = ref.forward_bounds()
+    o64.check(out, ref.out, bo, "out")
+    o64.check(lse, ref.lse, bl, "lse")
