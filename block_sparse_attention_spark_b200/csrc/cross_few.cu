@@ -7,9 +7,9 @@
 // through a ring of their own in shared memory (cp.async, no block barrier in
 // the loop): 16 KB per step at d = 128, two steps in flight per warp. Each warp keeps
 // the running maximum, sum and O of its keys; warps are joined in shared
-// memory. Up to eight blocks of a tile form a cluster and join over its shared
-// memory, each a part of the rows' values; more (fewer than 19 tiles on the
-// whole GPU) leave their shares in the workspace for join_kernel. Keys that are
+// memory. Up to eight blocks of a tile form a cluster, if all of those fit on the
+// GPU at once, and join over its shared memory, each a part of the rows' values;
+// more blocks leave their shares in the workspace for join_kernel. Keys that are
 // not kept are not read at all: cp.async fills their rows with zeros and their
 // logits are -inf.
 #include <cooperative_groups.h>
@@ -32,6 +32,7 @@ struct Args {
   int rows;                // G * Nq
   int tiles, splits;
   int stages;              // STAGES, or 1 where a warp has one step at most
+  int cluster;             // the splits of a tile are a cluster, which joins them
   int per_split;           // keys per split, a multiple of KEYS
   float* part;             // [tiles * B * Hkv][splits][16][d], then the (max, sum) pairs
   float2* stat;
@@ -82,10 +83,17 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return r;
 }
 template <bool H>
-__device__ __forceinline__ void put(char* dst, float v) {
-  if constexpr (H) *reinterpret_cast<__half*>(dst) = __float2half_rn(v);
-  else *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(v);
+__device__ __forceinline__ void put4(char* dst, const float4& v) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack<H>(v.x, v.y), pack<H>(v.z, v.w));
 }
+// v += f * x
+__device__ __forceinline__ void add4(float4& v, float f, const float4& x) {
+  v.x = fmaf(f, x.x, v.x);
+  v.y = fmaf(f, x.y, v.y);
+  v.z = fmaf(f, x.z, v.z);
+  v.w = fmaf(f, x.w, v.w);
+}
+__device__ __forceinline__ float4 times(const float4& v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
 
 template <int D, bool H>
 __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a) {
@@ -246,7 +254,6 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
     ss[warp * ROWS + r0 + 8] = make_float2(m[1], l[1]);
   }
   __syncthreads();
-  const bool cluster_join = a.splits > 1 && a.splits <= CLUSTER;
   float* wf = so + WARPS * ROWS * D + 2 * WARPS * ROWS;                 // [WARPS][ROWS] weights of the join
   float2* js = reinterpret_cast<float2*>(wf + WARPS * ROWS);          // [ROWS] the block's statistics
   float* jo = reinterpret_cast<float*>(js + ROWS);                      // [ROWS][D] its O, for its cluster
@@ -277,38 +284,40 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) wf[w * ROWS + tid] = f[w] * norm;
     js[tid] = make_float2(mm, ll);
-    if (a.splits > CLUSTER) a.stat[part * ROWS + tid] = make_float2(mm, ll);
+    if (a.splits > 1 && !a.cluster) a.stat[part * ROWS + tid] = make_float2(mm, ll);
     if (a.splits == 1) write_lse(tid, mm, ll);
   }
   __syncthreads();
+  // four values a thread at a time
 #pragma unroll 4
-  for (int i = tid; i < live * D; i += THREADS) {
+  for (int i = 4 * tid; i < live * D; i += 4 * THREADS) {
     const int r = i / D, c = i % D;
-    float v = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) v += wf[w * ROWS + r] * so[(w * ROWS + r) * D + c];
-    if (cluster_join) {
-      jo[i] = v;
+    for (int w = 0; w < WARPS; ++w) add4(v, wf[w * ROWS + r], *reinterpret_cast<const float4*>(so + (w * ROWS + r) * D + c));
+    if (a.cluster) {
+      *reinterpret_cast<float4*>(jo + i) = v;
     } else if (a.splits > 1) {
-      a.part[part * ROWS * D + i] = v;
+      *reinterpret_cast<float4*>(a.part + part * ROWS * D + i) = v;
     } else {
       int h, n;
       out_row(r, h, n);
-      put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), v);
+      put4<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), v);
     }
   }
-  if (cluster_join) {
+  if (a.cluster) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();       // (1, splits, 1): rank = split
     cluster.sync();
-    for (int i = split * THREADS + tid; i < live * D; i += a.splits * THREADS) {
+    for (int i = 4 * (split * THREADS + tid); i < live * D; i += 4 * a.splits * THREADS) {
       const int r = i / D, c = i % D;
       float2 st[CLUSTER];
-      float x[CLUSTER], mm = -INFINITY, ll = 0.f, v = 0.f;
+      float4 x[CLUSTER], v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mm = -INFINITY, ll = 0.f;
 #pragma unroll
       for (int k = 0; k < CLUSTER; ++k) {                 // all on their way at once
         st[k] = k < a.splits ? *cluster.map_shared_rank(js + r, k) : make_float2(-INFINITY, 0.f);
-        x[k] = k < a.splits ? *cluster.map_shared_rank(jo + i, k) : 0.f;
+        x[k] = k < a.splits ? *cluster.map_shared_rank(reinterpret_cast<float4*>(jo + i), k) : v;
       }
 #pragma unroll
       for (int k = 0; k < CLUSTER; ++k) mm = fmaxf(mm, st[k].x);
@@ -316,36 +325,54 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
       for (int k = 0; k < CLUSTER; ++k) {
         const float f = st[k].x == -INFINITY ? 0.f : exp2f(st[k].x - mm);
         ll += f * st[k].y;
-        v += f * x[k];
+        add4(v, f, x[k]);
       }
       int h, n;
       out_row(r, h, n);
-      put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll == 0.f ? 0.f : v / ll);
+      put4<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), times(v, ll == 0.f ? 0.f : 1.f / ll));
       if (c == 0) write_lse(r, mm, ll);
     }
     cluster.sync();                                       // no block leaves while another reads its shared memory
   }
 }
 
-// Joins the splits of a row: grid (rows, B * Hkv), one thread per value.
+// Joins the splits of a row: grid (rows, B * Hkv). D / 4 threads have the row's
+// values, 4 groups (d = 64: 8) of them a share each of the splits, added in
+// shared memory in order.
 template <int D, bool H>
-__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(THREADS) join_kernel(const __grid_constant__ Args a) {
+  constexpr int LANES = D / 4, GROUPS = THREADS / LANES;
+  __shared__ float4 sum[GROUPS][LANES];
+  __shared__ float den[GROUPS];
   const Problem& p = a.p;
-  const int row = blockIdx.x, bk = blockIdx.y, c = threadIdx.x;
+  const int row = blockIdx.x, bk = blockIdx.y, x = threadIdx.x % LANES, y = threadIdx.x / LANES, c = 4 * x;
   const int b = bk / p.Hkv, hk = bk % p.Hkv;
   const size_t unit = (size_t)bk * a.tiles + row / ROWS;
   const int r = row % ROWS;
-  float mm = -INFINITY, ll = 0.f, v = 0.f;
-  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.stat[(unit * a.splits + s) * ROWS + r].x);
+  float mm = -INFINITY, ll = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = x; s < a.splits; s += LANES) mm = fmaxf(mm, a.stat[(unit * a.splits + s) * ROWS + r].x);
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
   const float ref = mm == -INFINITY ? 0.f : mm;
-  for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+  for (int s = y; s < a.splits; s += GROUPS) {
     const float2 st = a.stat[(unit * a.splits + s) * ROWS + r];
     const float f = exp2f(st.x - ref);
     ll += f * st.y;
-    v += f * a.part[((unit * a.splits + s) * ROWS + r) * D + c];
+    add4(v, f, *reinterpret_cast<const float4*>(a.part + ((unit * a.splits + s) * ROWS + r) * D + c));
+  }
+  sum[y][x] = v;
+  if (x == 0) den[y] = ll;
+  __syncthreads();
+  if (y != 0) return;
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) {
+    add4(v, 1.f, sum[i][x]);
+    ll += den[i];
   }
   const int g = row / p.Nq, n = row % p.Nq, h = hk * p.G + g;
-  put<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), ll == 0.f ? 0.f : v / ll);
+  put4<H>(p.out.data + 2 * (b * p.out.b + h * p.out.h + n * p.out.n + c), times(v, ll == 0.f ? 0.f : 1.f / ll));
   if (c == 0 && p.lse != nullptr)
     p.lse[((size_t)b * p.Hq + h) * p.Nq + n] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
 }
@@ -360,19 +387,15 @@ static Args plan(const Problem& p, void* ws) {
   // memory); or, where that many clusters of blocks fit at two an SM, down to one step
   // a warp, which needs no ring (one token over 512 keys, 64 heads: 4 blocks a head)
   const int64_t most = (p.Nk + MIN_KEYS - 1) / MIN_KEYS;
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(most, SM_COUNT / units));
-  a.stages = STAGES;
-  if (most <= CLUSTER && units * most <= 2 * SM_COUNT) {
-    splits = most;
-  } else if (splits > 2 && splits <= CLUSTER) {
-    // clusters of three or five leave SMs of a GPC empty and wait for a second
-    // round, and so do 16 clusters of eight (37 us where a first round takes 15)
-    splits = splits == CLUSTER && units * CLUSTER <= 64 ? CLUSTER : splits >= 4 ? 4 : 2;
-    if (splits == 4 && units * splits > 128) splits = 2;
-  }
-  a.per_split = (int)(((p.Nk + splits - 1) / splits + MIN_KEYS - 1) / MIN_KEYS * MIN_KEYS);
+  const bool short_keys = most <= CLUSTER && units * most <= ((most & (most - 1)) == 0 ? 2 : 1) * SM_COUNT;
+  const int64_t want = short_keys ? most : std::max<int64_t>(1, std::min<int64_t>(most, SM_COUNT / units));
+  a.per_split = (int)((most + want - 1) / want) * MIN_KEYS;
   a.splits = (p.Nk + a.per_split - 1) / a.per_split;
-  if (a.per_split == MIN_KEYS) a.stages = 1;
+  a.stages = a.per_split == MIN_KEYS ? 1 : STAGES;
+  // Clusters that do not fit in one round (16 of eight blocks: 37 us where the first
+  // round takes 15; sizes between leave SMs of a GPC empty) are no clusters
+  a.cluster = a.splits > 1 && a.splits <= CLUSTER &&
+              (short_keys || a.splits == 2 || units * a.splits <= (a.splits > 4 ? 64 : 128));
   a.part = static_cast<float*>(ws);
   a.stat = reinterpret_cast<float2*>(a.part + units * a.splits * ROWS * p.d);
   return a;
@@ -393,10 +416,10 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
   attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
   attr.val.clusterDim.y = a.splits;
   cfg.attrs = &attr;
-  cfg.numAttrs = a.splits > 1 && a.splits <= CLUSTER ? 1 : 0;
+  cfg.numAttrs = a.cluster;
   const cudaError_t l = cudaLaunchKernelEx(&cfg, kernel<D, H>, a);
   if (l != cudaSuccess) return l;
-  if (a.splits > CLUSTER) join_kernel<D, H><<<dim3(a.rows, a.p.B * a.p.Hkv), D, 0, s>>>(a);
+  if (a.splits > 1 && !a.cluster) join_kernel<D, H><<<dim3(a.rows, a.p.B * a.p.Hkv), THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -404,7 +427,7 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
 
 size_t few_workspace(const Problem& p) {
   const few::Args a = few::plan(p, nullptr);
-  return a.splits > few::CLUSTER ? (size_t)a.tiles * p.B * p.Hkv * a.splits * few::ROWS * (p.d * sizeof(float) + sizeof(float2)) : 0;
+  return a.splits > 1 && !a.cluster ? (size_t)a.tiles * p.B * p.Hkv * a.splits * few::ROWS * (p.d * sizeof(float) + sizeof(float2)) : 0;
 }
 
 cudaError_t launch_few(const Problem& p, void* ws, cudaStream_t s) {

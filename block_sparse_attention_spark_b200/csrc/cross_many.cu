@@ -509,31 +509,49 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
-// Joins the shares of a row: grid (row tiles * 16, B * Hkv), a warp per row.
-template <int D, bool H>
+// Joins the shares of a row: WARPS warps a row, 8 / WARPS rows a block, grid (row
+// tiles * 128 rows, B * Hkv). One warp reads up to 16 shares in a few latencies; of
+// 74, eight warps read ten each.
+template <int D, bool H, int WARPS>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
-  const int t = blockIdx.x / 16, bk = blockIdx.y, lane = threadIdx.x & 31;
+  constexpr int PER = 8 / WARPS, BLOCKS = ROWS / PER, V = D / 32;
+  __shared__ float stat[8];
+  __shared__ float sum[8][D];
+  const int t = blockIdx.x / BLOCKS, bk = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = bk / a.Hkv, hk = bk % a.Hkv;
   const int g = t / a.tokens, h = hk * a.G + g;
   const size_t first = ((size_t)bk * a.pairs + t / 2) * a.splits;    // item of share 0
-  const int r = (blockIdx.x % 16) * 8 + (threadIdx.x >> 5), n = (t % a.tokens) * ROWS + r;
-  if (n >= a.Nq) return;
+  const int r = (blockIdx.x % BLOCKS) * PER + warp / WARPS, n = (t % a.tokens) * ROWS + r;
+  if (n >= a.Nq) return;                     // (with several warps a row, the whole block)
   auto row = [&](int s) { return ((first + s) * SLOTS + (t & 1)) * ROWS + r; };
   float m = -INFINITY;
   for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.stat[row(s)].x);
   m = warp_maxf(m);
-  float l = 0.f, o[D / 32];
+  float l = 0.f, o[V];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+  for (int e = 0; e < V; ++e) o[e] = 0.f;
   const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = warp % WARPS; s < a.splits; s += WARPS) {
     const float2 st = a.stat[row(s)];
     const float f = exp2f(st.x - ref);
     l += f * st.y;
-    const float* src = a.part + row(s) * D + lane * (D / 32);
+    const float* src = a.part + row(s) * D + lane * V;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
+    for (int e = 0; e < V; ++e) o[e] = fmaf(f, src[e], o[e]);
+  }
+  if constexpr (WARPS > 1) {
+    stat[warp] = l;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[warp][lane * V + e] = o[e];
+    __syncthreads();
+    if (warp % WARPS != 0) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      l += stat[warp + w];
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] += sum[warp + w][lane * V + e];
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   char* dst = a.out.data + 2 * (b * a.out.b + h * a.out.h + (int64_t)n * a.out.n) + lane * (D / 16);
@@ -566,7 +584,9 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
   const cudaError_t e = allow_shared(kernel<D, H>, Lay<D>::SMEM, &done);
   if (e != cudaSuccess) return e;
   kernel<D, H><<<std::min(a.items, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
-  if (a.splits > 1) join_kernel<D, H><<<dim3(a.G * a.tokens * (ROWS / 8), a.B * a.Hkv), 256, 0, s>>>(a);
+  const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+  if (a.splits > 32 || (a.splits > 4 && rows <= 8 * SM_COUNT)) join_kernel<D, H, 8><<<dim3(a.G * a.tokens * ROWS, a.B * a.Hkv), 256, 0, s>>>(a);
+  else if (a.splits > 1) join_kernel<D, H, 1><<<dim3(a.G * a.tokens * (ROWS / 8), a.B * a.Hkv), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
