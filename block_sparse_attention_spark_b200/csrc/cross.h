@@ -21,11 +21,13 @@ struct Problem {
 
 // Few query rows: 16 rows per tile (mma.sync), keys split over warps and blocks.
 size_t few_workspace(const Problem& p);
+void few_keys(const Problem& p, int64_t* keys);   // keys of an SM's blocks one after another, 256 for the start of each
 cudaError_t launch_few(const Problem& p, void* ws, cudaStream_t s);
 
 // Many query rows: 128 rows per tile (tcgen05). Kept keys are the first
 // key_len[b] of an item; key_mask is not looked at.
 size_t many_workspace(const Problem& p);
+void many_keys(const Problem& p, int64_t* keys, int* shares);   // keys of a CTA's items, shares of a row tile
 cudaError_t launch_many(const Problem& p, void* ws, cudaStream_t s);
 
 // The kept keys of each item moved to the front: k and v become contiguous

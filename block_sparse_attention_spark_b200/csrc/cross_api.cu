@@ -29,16 +29,24 @@ static Problem problem(const spark_cross_params* p) {
   return c;
 }
 
-// Rows of a key head (query heads of its group times tokens): up to one tile of
-// 16 always by the few-row kernel, which reads K and V once; more as long as
-// all its tiles together read few enough keys (each tile reads them again), else by the tensor-core
-// kernel's tiles of 128 rows of a head. Measured on both sides of the rule, few
-// against many: d = 128, 512 keys, 16 heads: 32 rows 8.7 / 9.5 us, 64 rows 10.1 /
-// 10.0, 128 rows 12.1 / 11.0; 2 key heads of 2048 keys: 64 rows 9.8 / 14.6, 128
-// rows 17.7 / 14.7; d = 64, 16 key heads of 333 keys: 192 rows 7.8 / 11.2, 384 rows 12.5 / 12.6.
+// Up to 16 rows of a key head (query heads of its group times tokens), one tile:
+// always the few-row kernel, which reads K and V once. More: the kernel whose
+// estimate is less, both in keys' time of the few-row kernel (about 11.5 ns at
+// d = 128, 6 at 64): keys a block works on, plus what starting a block, cutting
+// the keys into shares and reading the first tile cost. Measured on both sides,
+// few / many, us: d = 128: 16 heads of 512 keys: 32 rows 6.6 / 9.3, 64 8.0 / 10.1,
+// 128 10.8 / 11.1, 256 19.3 / 14.2; 8 heads of 8192: 16 rows 13.6 / 17.8, 32 19.2 /
+// 17.8, 128 51 / 21; 256 heads of 77: 32 rows 6.3 / 7.3, 64 11.1 / 7.3; one key head
+// of 16384: 64 rows 14.5 / 16.6, 128 19.2 / 16.5. d = 64: 160 heads of 512: 32 rows
+// 12.0 / 16.0, 64 18.3 / 16.6; 2 key heads of 2048: 512 rows 10.8 / 13.1, 768 14.8 / 13.2.
 static bool few_rows(const Problem& c) {
-  const int64_t rows = (int64_t)c.G * c.Nq, tiles = (rows + 15) / 16 * c.B * c.Hkv;
-  return rows <= 16 || (tiles <= 2 * SM_COUNT && tiles * c.Nk <= (c.d == 128 ? 24576 : 98304));
+  if ((int64_t)c.G * c.Nq <= 16) return true;
+  int64_t few, many;
+  int shares;
+  few_keys(c, &few);
+  many_keys(c, &many, &shares);
+  if (c.d == 128) return few <= 300 + many + (shares > 1 ? 220 + 8 * std::min(shares, 32) : 0);
+  return few <= 450 + many * 8 / 5 + (shares > 1 ? 600 + 15 * std::min(shares, 24) : 0);
 }
 
 // With a key mask the tensor-core kernels get the kept keys packed to the

@@ -430,6 +430,13 @@ size_t few_workspace(const Problem& p) {
   return a.splits > 1 && !a.cluster ? (size_t)a.tiles * p.B * p.Hkv * a.splits * few::ROWS * (p.d * sizeof(float) + sizeof(float2)) : 0;
 }
 
+void few_keys(const Problem& p, int64_t* keys) {
+  const few::Args a = few::plan(p, nullptr);
+  const int at_once = (p.d == 128 ? 1 : 2) + (a.stages == 1);       // blocks an SM holds
+  const int64_t blocks = (int64_t)a.tiles * p.B * p.Hkv * a.splits, wave = (int64_t)at_once * SM_COUNT;
+  *keys = (blocks + wave - 1) / wave * (a.per_split + 256);
+}
+
 cudaError_t launch_few(const Problem& p, void* ws, cudaStream_t s) {
   const few::Args a = few::plan(p, ws);
   if (p.d == 128) return p.fp16 ? few::run<128, true>(a, s) : few::run<128, false>(a, s);

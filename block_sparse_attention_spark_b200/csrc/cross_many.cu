@@ -598,6 +598,14 @@ size_t many_workspace(const Problem& p) {
   return many::workspace(p, a);
 }
 
+void many_keys(const Problem& p, int64_t* keys, int* shares) {
+  many::Args a = {};
+  many::plan(p, &a);
+  const int tiles = (p.Nk + many::KEYS - 1) / many::KEYS;
+  *keys = (int64_t)((a.items + SM_COUNT - 1) / SM_COUNT) * ((tiles + a.splits - 1) / a.splits) * many::KEYS;
+  *shares = a.splits;
+}
+
 cudaError_t launch_many(const Problem& p, void* ws, cudaStream_t s) {
   many::Args a = {};
   many::plan(p, &a);
