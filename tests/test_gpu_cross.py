@@ -200,3 +200,73 @@ def test_cross_attention_mask_of_many_keys():
     bo, bl = ref.forward_bounds()
     o64.check(out, ref.out, bo, "out")
     o64.check(lse, ref.lse, bl, "lse")
+
+
+# many rows of many heads: the tensor-core kernel (the same lengths at few heads are the few-row kernel's)
+MANY = [
+    (4, 40, 40, 129, 65, 128, "bf16", "mask"),
+    (8, 40, 20, 200, 64, 64, "fp16", "none"),
+    (2, 60, 60, 255, 127, 128, "fp16", "lengths"),
+    (8, 48, 16, 333, 129, 64, "bf16", "lengths mask"),
+    (1, 80, 80, 300, 257, 128, "bf16", "none"),
+    (16, 30, 15, 257, 333, 128, "bf16", "empty"),
+    (2, 200, 200, 150, 1, 128, "fp16", "none"),
+    (3, 150, 150, 200, 2, 64, "bf16", "lengths"),
+    (5, 70, 70, 131, 17, 128, "bf16", "mask"),
+    (6, 32, 4, 100, 300, 64, "fp16", "mask"),
+    (1, 3, 1, 400, 4000, 128, "fp16", "lengths mask"),
+    (1, 12, 12, 2000, 640, 64, "bf16", "none"),
+]
+
+
+@pytest.mark.parametrize("c", MANY, ids=ids)
+def test_cross_attention_many_rows(c):
+    p = spark.cross_params(*c[:2], *c[3:6], heads_kv=c[2], dtype=c[6])
+    assert spark.cross_workspace_size(p) >= 4 * c[0] * c[2] * c[4] * c[5]      # room for packed keys
+    test_cross_attention(c)
+
+
+def test_cross_attention_many_rows_lowest_values():
+    """Keys of the type's lowest value (logits overflow to -inf), alone and beside others, in the tensor-core kernel."""
+    for low in (0, 200):
+        p, q, k, v, _ = inputs(1, 120, 120, 300, 300, 128)
+        q, k = q.abs(), k.clone()
+        k[:, :, low:] = torch.finfo(torch.bfloat16).min
+        got, lse = spark.cross_attn(p, q, k, v, return_lse=True)
+        assert spark.get_status() == 0
+        if low == 0:
+            assert (got == 0).all() and torch.isneginf(lse).all()
+        else:
+            want = o64.Cross(q, k[:, :, :low], v[:, :, :low])
+            o64.check(got, want.out, want.forward_bounds()[0], "out")
+
+
+def test_cross_attention_many_rows_layouts_streams_and_graphs():
+    p, q, k, v, kw = inputs(4, 40, 20, 130, 99, 64, mask="lengths mask")
+    want = spark.cross_attn(p, q, k, v, **kw)
+    big = torch.full((4, 133, 42, 64), 7.0, dtype=q.dtype, device="cuda")
+    view = big[:, 1:131, 1:41].transpose(1, 2)
+    spark.cross_attn(p, q, k, v, out=view, **kw)
+    assert torch.equal(view, want)
+    big[:, 1:131, 1:41] = 7.0
+    assert (big == 7.0).all()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = spark.cross_attn(p, q, k, v, **kw)
+    s.synchronize()
+    assert torch.equal(got, want)
+    ws = spark.alloc_cross_workspace(p)
+    outs, graphs = [], []
+    for x in (q, (q * 0.5).clone()):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((x, spark.cross_attn(p, x, k, v, ws=ws, **kw)))
+        graphs.append(g)
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for x, o in outs:
+        assert torch.equal(o, spark.cross_attn(p, x, k, v, **kw))
+    assert spark.get_status() == 0
