@@ -69,6 +69,7 @@ template <int D>
 __global__ void __launch_bounds__(256) stat_kernel(const __grid_constant__ Args a, const __grid_constant__ PackArgs pack,
                                                   int per_head, int blocks) {
   constexpr int LPR = D / 8, ROWS = 256 / LPR;
+  let_next_start();
   if ((int)blockIdx.x >= blocks) {
     pack_block(pack, blockIdx.x - blocks);
     return;
@@ -186,6 +187,7 @@ __device__ __forceinline__ bool start(unsigned char* smem, int nbar, const unsig
   __syncthreads();
   fence_after();
   k.tmem = __shfl_sync(0xffffffffu, words[0], 0);
+  wait_for_last();
   return true;
 }
 __device__ __forceinline__ void finish(const Block& k) {
@@ -741,6 +743,8 @@ __global__ void __launch_bounds__(THREADS, 1) main_kernel(const __grid_constant_
 // 128 threads of a block dV, the upper ones dK. grid (keys / (1024 / d), Hkv, B).
 template <int D>
 __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ Args a) {
+  wait_for_last();
+  let_next_start();
   const int hk = blockIdx.y, b = blockIdx.z, y = threadIdx.x >> 7, x = threadIdx.x & 127;
   const int n = blockIdx.x * (1024 / D) + x / (D / 8), c = 8 * (x % (D / 8));
   if (n >= a.Nk) return;
@@ -769,6 +773,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ Args a
 // dQ where a query tile's keys were split: four values a thread. grid (queries / (1024 / d), B * Hq).
 template <int D>
 __global__ void __launch_bounds__(256) sum_rows_kernel(const __grid_constant__ Args a) {
+  wait_for_last();
   const int bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
   const int n = blockIdx.x * (1024 / D) + threadIdx.x / (D / 4), c = 4 * (threadIdx.x % (D / 4));
   if (n >= a.Nq) return;
@@ -839,10 +844,13 @@ static cudaError_t run(const Args& a, const PackArgs& pack, cudaStream_t s) {
   const int64_t stat_blocks = (int64_t)per_head * a.B * a.Hq, all = stat_blocks + pack_blocks(pack);
   if (all > INT32_MAX) return cudaErrorInvalidValue;
   stat_kernel<D><<<(unsigned)all, 256, 0, s>>>(a, pack, per_head, (int)stat_blocks);
-  main<<<row_blocks + std::min(a.kitems, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a, row_blocks);
-  sum_kernel<D><<<dim3((a.Nk * (D / 64) + 15) / 16, a.Hkv, a.B), 256, 0, s>>>(a);
-  if (a.qsplits > 1) sum_rows_kernel<D><<<dim3((a.Nq * (D / 64) + 15) / 16, a.B * a.Hq), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaError_t l = cudaGetLastError();
+  if (l == cudaSuccess)
+    l = launch_behind(main, dim3(row_blocks + std::min(a.kitems, SM_COUNT)), THREADS, Lay<D>::SMEM, s, a, row_blocks);
+  if (l == cudaSuccess) l = launch_behind(sum_kernel<D>, dim3((a.Nk * (D / 64) + 15) / 16, a.Hkv, a.B), 256, 0, s, a);
+  if (l == cudaSuccess && a.qsplits > 1)
+    l = launch_behind(sum_rows_kernel<D>, dim3((a.Nq * (D / 64) + 15) / 16, a.B * a.Hq), 256, 0, s, a);
+  return l;
 }
 
 }  // namespace bwd

@@ -99,6 +99,7 @@ template <int D, bool H>
 __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a) {
   using L = Lay<D>;
   constexpr int CH = D / 8;                  // 16-byte chunks of a row
+  let_next_start();
   extern __shared__ __align__(128) unsigned char smem[];
   const Problem& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const __grid_constant__ A
   constexpr int LANES = D / 4, GROUPS = THREADS / LANES;
   __shared__ float4 sum[GROUPS][LANES];
   __shared__ float den[GROUPS];
+  wait_for_last();
   const Problem& p = a.p;
   const int row = blockIdx.x, bk = blockIdx.y, x = threadIdx.x % LANES, y = threadIdx.x / LANES, c = 4 * x;
   const int b = bk / p.Hkv, hk = bk % p.Hkv;
@@ -419,8 +421,8 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
   cfg.numAttrs = a.cluster;
   const cudaError_t l = cudaLaunchKernelEx(&cfg, kernel<D, H>, a);
   if (l != cudaSuccess) return l;
-  if (a.splits > 1 && !a.cluster) join_kernel<D, H><<<dim3(a.rows, a.p.B * a.p.Hkv), THREADS, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.splits == 1 || a.cluster) return cudaSuccess;
+  return launch_behind(join_kernel<D, H>, dim3(a.rows, a.p.B * a.p.Hkv), THREADS, 0, s, a);
 }
 
 }  // namespace few

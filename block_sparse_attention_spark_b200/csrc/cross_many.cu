@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
   fence_before();
   __syncthreads();
   fence_after();
+  wait_for_last();
+  let_next_start();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_sh, 0);
   const int row_tiles = a.G * a.tokens;
 
@@ -517,6 +519,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   constexpr int PER = 8 / WARPS, BLOCKS = ROWS / PER, V = D / 32;
   __shared__ float stat[8];
   __shared__ float sum[8][D];
+  wait_for_last();
   const int t = blockIdx.x / BLOCKS, bk = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = bk / a.Hkv, hk = bk % a.Hkv;
   const int g = t / a.tokens, h = hk * a.G + g;
@@ -583,11 +586,12 @@ static cudaError_t run(const Args& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(kernel<D, H>, Lay<D>::SMEM, &done);
   if (e != cudaSuccess) return e;
-  kernel<D, H><<<std::min(a.items, SM_COUNT), THREADS, Lay<D>::SMEM, s>>>(a);
+  const cudaError_t l = launch_behind(kernel<D, H>, dim3(std::min(a.items, SM_COUNT)), THREADS, Lay<D>::SMEM, s, a);
+  if (l != cudaSuccess || a.splits == 1) return l;
   const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
-  if (a.splits > 32 || (a.splits > 4 && rows <= 8 * SM_COUNT)) join_kernel<D, H, 8><<<dim3(a.G * a.tokens * ROWS, a.B * a.Hkv), 256, 0, s>>>(a);
-  else if (a.splits > 1) join_kernel<D, H, 1><<<dim3(a.G * a.tokens * (ROWS / 8), a.B * a.Hkv), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.splits > 32 || (a.splits > 4 && rows <= 8 * SM_COUNT)) 
+    return launch_behind(join_kernel<D, H, 8>, dim3(a.G * a.tokens * ROWS, a.B * a.Hkv), 256, 0, s, a);
+  return launch_behind(join_kernel<D, H, 1>, dim3(a.G * a.tokens * (ROWS / 8), a.B * a.Hkv), 256, 0, s, a);
 }
 
 }  // namespace many

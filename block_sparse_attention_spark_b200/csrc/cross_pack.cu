@@ -5,7 +5,10 @@
 namespace spark {
 namespace cross {
 
-__global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constant__ PackArgs a) { pack_block(a, blockIdx.x); }
+__global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constant__ PackArgs a) {
+  let_next_start();
+  pack_block(a, blockIdx.x);
+}
 
 Packed pack_plan(const Problem& p) {
   const size_t rows = (size_t)p.B * p.Hkv * p.Nk;

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(THREADS, BWD && NORMED ? 3 : 4) kernel(const _
       heads<T, D, MODE, BWD, false>(t, b, n, h0, h1, l, a.npairs, a.eps, c, s, live, active, dw);
   }
   if constexpr (BWD && NORMED) {
+    let_next_start();
     // this block's sums of dw: tokens of a warp by shuffles, warps in shared memory, a fixed order
     if (t.weight == nullptr) return;
     __shared__ float sh[THREADS / 32][D];
@@ -383,6 +384,7 @@ __global__ void __launch_bounds__(THREADS, BWD && NORMED ? 3 : 4) kernel(const _
 __global__ void __launch_bounds__(256) sum_kernel(const float* __restrict__ part, int blocks_q, int blocks, int d,
                                                   float* __restrict__ dwq, float* __restrict__ dwk) {
   __shared__ double sh[32][9];
+  wait_for_last();
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
   const int col = blockIdx.x * 8 + x;
   float* dst = blockIdx.y ? dwk : dwq;
@@ -578,10 +580,9 @@ spark_status spark_rotary_bwd(const spark_rotary_params* p, const spark_view* dq
   const spark_status e = norm ? rotary::launch<true, true>(p, (int)blocks, a, stream)
                               : rotary::launch<true, false>(p, (int)blocks, a, stream);
   if (e != SPARK_OK || !norm) return e;
-  rotary::sum_kernel<<<dim3(p->d / 8, 2), 256, 0, stream>>>(a.part, a.blocks_q, (int)blocks, p->d,
-                                                            weights[0] ? dq_weight : nullptr,
-                                                            weights[1] ? dk_weight : nullptr);
-  return cudaGetLastError() == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  const cudaError_t l = launch_behind(rotary::sum_kernel, dim3(p->d / 8, 2), 256, 0, stream, a.part, a.blocks_q, (int)blocks,
+                                      p->d, weights[0] ? dq_weight : nullptr, weights[1] ? dk_weight : nullptr);
+  return l == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
 size_t spark_forward_rotary_workspace_size(const spark_params* p) {

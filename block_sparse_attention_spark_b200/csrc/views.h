@@ -64,6 +64,29 @@ inline cudaError_t allow_shared(F* kernel, int bytes, std::atomic<uint64_t>* don
   return e;
 }
 
+// A launch that may be set up while the stream's last kernel (one that calls
+// let_next_start) still runs; the kernel begins with wait_for_last.
+template <typename... P, typename... A>
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, int shared, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Returns once the kernel before has ended and what it wrote is visible; nothing
+// in global memory is touched before it.
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 // The library's device status word on the current device (spark_get_status).
 int* device_status();
 
