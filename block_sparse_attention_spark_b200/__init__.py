@@ -423,6 +423,14 @@ def _view(t, name, dev, dtype, shape):
     raise _wrong(t, name, dev, dtype, shape, "a (last axis contiguous)")
 
 
+def _made(t):
+    """View of a tensor made here like one that _view has looked at."""
+    b, h, n, one = t.stride()
+    if one != 1:
+        raise RuntimeError(f"a result's last axis has stride {one}")
+    return View(t.data_ptr(), b, h, n)
+
+
 def _device(t, name):
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -512,10 +520,11 @@ def rotary(p: RotaryParams, q, k=None, positions=None, q_weight=None, k_weight=N
     if out is None:
         qo = torch.empty_like(q, memory_format=torch.contiguous_format)
         ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+        wqo, wko = _made(qo), None if k is None else _made(ko)
     else:
         qo, ko = out
-    wqo = _view(qo, "q_out", dev, dt, qs)
-    wko = None if k is None else _view(ko, "k_out", dev, dt, ks)
+        wqo = _view(qo, "q_out", dev, dt, qs)
+        wko = None if k is None else _view(ko, "k_out", dev, dt, ks)
     _call(lib().spark_rotary, "spark_rotary", dev, p, vq, vk, pos, wq, wk, wqo, wko)
     return qo, ko
 
@@ -546,8 +555,7 @@ def rotary_bwd(p: RotaryParams, dq_out, dk_out=None, q=None, k=None, positions=N
         ws = _scratch(ws, lambda: rotary_workspace_size(p), dev, "rotary_bwd")
     else:
         ws = None
-    odq = _view(dq, "dq", dev, dt, qs)
-    odk = None if dk is None else _view(dk, "dk", dev, dt, ks)
+    odq, odk = _made(dq), None if dk is None else _made(dk)
     _call(lib().spark_rotary_bwd, "spark_rotary_bwd", dev, p, gq, gk, vq, vk, pos, wq, wk, odq, odk, _ptr(dwq),
           _ptr(dwk), _ptr(ws), 0 if ws is None else ws.numel())
     return dq, dk, dwq, dwk
@@ -621,7 +629,9 @@ def cross_attn(p: CrossParams, q, k, v, ws=None, key_len=None, key_mask=None, re
     kl, km = _cross_masks(p, dev, key_len, key_mask)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    vo = _view(out, "out", dev, dt, qs)
+        vo = _made(out)
+    else:
+        vo = _view(out, "out", dev, dt, qs)
     lse = q.new_empty(qs[:3], dtype=_dtype_of(2)) if return_lse else None
     ws = _scratch(ws, lambda: cross_workspace_size(p), dev, "cross_attn")
     _call(lib().spark_cross_attn, "spark_cross_attn", dev, p, vq, vk, vv, kl, km, vo, _ptr(lse), ws.data_ptr(),
@@ -640,7 +650,7 @@ def cross_attn_bwd(p: CrossParams, q, k, v, out, lse, dout, ws=None, key_len=Non
     pl = _on(lse, "lse", dev, _dtype_of(2), qs[:3])
     kl, km = _cross_masks(p, dev, key_len, key_mask)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    grads = [_view(t, n, dev, dt, s) for t, n, s in ((dq, "dq", qs), (dk, "dk", ks), (dv, "dv", ks))]
+    grads = [_made(t) for t in (dq, dk, dv)]
     ws = _scratch(ws, lambda: cross_workspace_size(p, True), dev, "cross_attn_bwd")
     _call(lib().spark_cross_attn_bwd, "spark_cross_attn_bwd", dev, p, *views[:4], pl, views[4], kl, km, *grads,
           ws.data_ptr(), ws.numel())

@@ -49,11 +49,12 @@ static bool few_rows(const Problem& c) {
   return few <= 450 + many * 8 / 5 + (shares > 1 ? 600 + 15 * std::min(shares, 24) : 0);
 }
 
-// With a key mask the tensor-core kernels get the kept keys packed to the
-// front (the masks of a call are not known here: the size covers both).
-static size_t forward_workspace(const Problem& c) {
-  return few_rows(c) ? few_workspace(c) : align_up(many_workspace(c)) + pack_plan(c).bytes;
-}
+// Workspace: what the kernels themselves need, and behind it room for the kept
+// keys of a masked call, packed to the front for the tensor-core kernels (the
+// size covers calls with and without a mask).
+static size_t forward_bytes(const Problem& c, bool few) { return few ? few_workspace(c) : align_up(many_workspace(c)); }
+static size_t backward_bytes(const Problem& c) { return align_up(bwd_workspace(c)); }
+static size_t total_bytes(const Problem& c, size_t own, bool packs) { return own + (packs ? pack_plan(c).bytes : 0) + 256; }
 
 // What packing a masked problem's keys into ws takes; the problem is then the packed one.
 static PackArgs pack(Problem* c, char* ws) {
@@ -80,7 +81,9 @@ spark_status spark_cross_validate(const spark_cross_params* p) { return cross::v
 size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd) {
   if (cross::validate(p) != SPARK_OK || (bwd && p->dtype != SPARK_BF16)) return 0;
   const cross::Problem c = cross::problem(p);
-  return (bwd ? cross::align_up(cross::bwd_workspace(c)) + cross::pack_plan(c).bytes : cross::forward_workspace(c)) + 256;
+  if (bwd) return cross::total_bytes(c, cross::backward_bytes(c), true);
+  const bool few = cross::few_rows(c);
+  return cross::total_bytes(c, cross::forward_bytes(c, few), !few);
 }
 
 spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, const spark_view* k,
@@ -95,13 +98,15 @@ spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, 
     return SPARK_ERR_INVALID_ARG;
   if (((uintptr_t)key_len & 3u) != 0 || ((uintptr_t)lse & 3u) != 0) return SPARK_ERR_INVALID_ARG;
   if (ws == nullptr || !aligned(ws)) return SPARK_ERR_INVALID_ARG;
-  if (ws_bytes < spark_cross_workspace_size(p, 0)) return SPARK_ERR_WORKSPACE;
+  const bool few = cross::few_rows(c);
+  const size_t own = cross::forward_bytes(c, few);
+  if (ws_bytes < cross::total_bytes(c, own, !few)) return SPARK_ERR_WORKSPACE;
   c.key_len = key_len;
   c.key_mask = key_mask;
   c.lse = lse;
   c.status = device_status();
-  if (cross::few_rows(c)) return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
-  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::many_workspace(c)));
+  if (few) return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + own);
   if (packed.mask != nullptr && cross::launch_pack(packed, stream) != cudaSuccess) return SPARK_ERR_CUDA;
   return cross::launch_many(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
@@ -124,12 +129,13 @@ spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view*
     return SPARK_ERR_INVALID_ARG;
   if (lse == nullptr || ((uintptr_t)lse & 3u) != 0 || ((uintptr_t)key_len & 3u) != 0) return SPARK_ERR_INVALID_ARG;
   if (ws == nullptr || !aligned(ws)) return SPARK_ERR_INVALID_ARG;
-  if (ws_bytes < spark_cross_workspace_size(p, 1)) return SPARK_ERR_WORKSPACE;
+  const size_t own = cross::backward_bytes(c);
+  if (ws_bytes < cross::total_bytes(c, own, true)) return SPARK_ERR_WORKSPACE;
   g.lse = lse;
   c.key_len = key_len;
   c.key_mask = key_mask;
   c.status = device_status();
-  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + cross::align_up(cross::bwd_workspace(c)));
+  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + own);
   return cross::launch_bwd(c, g, packed, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
