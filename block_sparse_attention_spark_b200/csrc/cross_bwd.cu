@@ -48,15 +48,110 @@ struct Args {
   int* status;
   int B, Hq, Hkv, G, Nq, Nk, NqP;            // NqP: Nq rounded up to 128
   int qtiles, ktiles;
-  int ksplits, kper, kitems;                 // shares of a key tile's query tiles, tiles per share
+  int ksplits, kper, kitems;                 // shares of a key tile's query tiles, tiles per share (unless dealt)
   int qsplits, qitems;                       // shares of a query tile's key tiles
-  int q_per;                                 // items of a CTA in a row; 0: every blocks-th
-  int stay;                                  // at most two key tiles: K stays in shared memory
+  int dealt;                                 // lengths, and more than one item a CTA: deal_out says who does what
+  int* deal;                                 // its shares of a key tile and (at 4) key tiles before each item of the batch
   float scale, sl2;
   float *lse2, *delta;                       // [B * Hq][NqP]
-  float* part;                               // [kitems][2][128][d] shares of dK and dV
+  float* part;                               // [key tiles (dealt: that have kept keys)][shares][2][128][d]: dV, dK
   float* qpart;                              // [qitems][128][d] shares of dQ
 };
+
+// ------------------------------------------------------------------ who does what
+// Shares of a key tile's L query tiles for `units` key tiles: the fewest of
+// those within 2% of the least time, in tiles: the rounds of items times the tiles
+// of an item and four more (its 128 KB of sums, written and read again, take about
+// that long), and 0.15 for each share that sum_kernel reads in turn.
+constexpr int KSLOTS = 6 * SM_COUNT;         // most shares in all, unless every tile has one
+__host__ __device__ inline int most_shares(int units, int L) {
+  const int s = units > 0 ? KSLOTS / units : KSLOTS;
+  return s < 1 ? 1 : s < L ? s : L;
+}
+__host__ __device__ inline float share_cost(int units, int L, int s) {
+  return (float)((L + s - 1) / s + 4) * (float)((units * s + SM_COUNT - 1) / SM_COUNT) + 0.15f * (float)s;
+}
+
+// What a CTA does: its items of dK and dV are `block`, block + blocks, ... below
+// kitems, those of dQ first, first + step, ... below end.
+struct Deal {
+  int ksplits, kper, kitems;
+  int b, before;                             // item of the batch of the CTA's first key tile, key tiles a head before that
+  int first, end, step;
+  int stay;                                  // no more than two key tiles: K stays in shared memory
+};
+
+// With lengths, which only the device knows, by one warp: key tiles without a
+// kept key are left out, so that the others are shared out evenly; query tiles go
+// to the CTAs in runs of equal weight, 1 for a key tile and 2 for the rest of an
+// item. 2 x 16,128 queries of 8 heads over 512 keys, of which 256 and 256 are kept:
+// 154 us (every blocks-th item, empty ones too, and no K that stays: 211); 500 and
+// 75: 202 (224 with weights 2 and 1; before 227). With one item a CTA at most there
+// is nothing to deal, and this would take 4 us (3 x 777 queries: 26 against 22).
+__device__ __forceinline__ void deal_out(const Args& a, bool rows, int block, int blocks, Deal* out) {
+  const int lane = threadIdx.x;
+  auto tiles = [&](int b) { return b < a.B ? (item_len(a.key_len, a.Nk, b, nullptr, false) + TILE - 1) / TILE : 0; };
+  const int mine = tiles(lane);
+  int sum = mine, top = mine;
+  for (int b = lane + 32; b < a.B; b += 32) {
+    sum += tiles(b);
+    top = max(top, tiles(b));
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  top = __reduce_max_sync(0xffffffffu, top);
+  Deal d = {};
+  const int units = a.Hkv * sum, L = a.G * a.qtiles, most = most_shares(units, L);
+  float least = INFINITY;
+  for (int s = 1 + lane; s <= most; s += 32) least = fminf(least, share_cost(units, L, s));
+  least = -warp_maxf(-least);
+  int pick = most;
+  for (int s = 1 + lane; s <= most; s += 32)
+    if (share_cost(units, L, s) <= least * 1.02f) pick = min(pick, s);
+  pick = __reduce_min_sync(0xffffffffu, pick);
+  d.kper = (L + pick - 1) / pick;
+  d.ksplits = (L + d.kper - 1) / d.kper;
+  d.kitems = units * d.ksplits;
+  d.stay = top <= 2 && a.qsplits == 1;
+  d.first = block;                           // shares of a query tile: every blocks-th
+  d.end = a.qitems;
+  d.step = blocks;
+  const int64_t per_item = (int64_t)a.Hq * a.qtiles, all = per_item * (sum + 2 * (int64_t)a.B);
+  const int64_t lo = all * block / blocks, hi = all * (block + 1) / blocks;
+  if (rows && a.qsplits == 1) {
+    d.step = 1;
+    d.first = a.qitems;
+  }
+  if (lane == 0) *out = d;
+  if (!rows && block == 0 && lane == 0) a.deal[0] = d.ksplits;
+  __syncwarp();
+  int run = 0;                               // key tiles of the items before
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane, t = b0 == 0 ? mine : tiles(b);
+    int inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const int before = run + inc - t;
+    run += __shfl_sync(0xffffffffu, inc, 31);
+    if (b >= a.B) continue;
+    if (rows) {
+      if (a.qsplits == 1) {
+        const int64_t w = t + 2, from = per_item * (before + 2 * (int64_t)b), to = from + per_item * w;
+        if (lo >= from && lo < to) out->first = (int)(b * per_item + (lo - from + w - 1) / w);
+        if (hi >= from && hi < to) out->end = (int)(b * per_item + (hi - from + w - 1) / w);
+      }
+    } else {
+      const int u = block / d.ksplits;
+      if (u >= a.Hkv * before && u < a.Hkv * (before + t)) {
+        out->b = b;
+        out->before = before;
+      }
+      if (block == 0) a.deal[4 + b] = before;
+    }
+  }
+}
 
 // ------------------------------------------------------------------ D and lse
 // 16 lanes (d = 128; 8 for 64) a row, four rows a lane in flight. Rows past Nq get
@@ -117,6 +212,7 @@ struct Lay {
   static constexpr int BYTES = ATOM * ATOMS;           // a tile of 128 rows
   static constexpr int OFF_ROW = (2 + STAGES) * BYTES; // two sets of lse and D of 128 queries
   static constexpr int OFF_BAR = OFF_ROW + 2048;
+  static constexpr int OFF_DEAL = OFF_BAR + 448;
   static constexpr int SMEM = OFF_BAR + 512;
   static_assert(SMEM <= 232448, "shared memory of a block");
 };
@@ -156,7 +252,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const TensorMap& m, int 
     tma_load_4d(dst + x * Lay<D>::ATOM, &m.map, 64 * x, n, m.h_on ? h : 0, m.b_on ? b : 0, bar);
 }
 
-// Shared start and end of both kernels.
+// Shared start and end of both bodies.
 struct Block {
   uint32_t base, bar0, tmem;
   int warp, lane;
@@ -207,7 +303,7 @@ __device__ __forceinline__ void finish(const Block& k) {
 // What stands in the rows of k and v past the kept ones only reaches their
 // own lanes, which are not written.
 template <int D>
-__device__ __forceinline__ void keys_body(const Args& a, unsigned char* smem, int block, int blocks) {
+__device__ __forceinline__ void keys_body(const Args& a, const Deal& deal, unsigned char* smem, int block, int blocks) {
   using L = Lay<D>;
   enum { FIXED_FULL, FIXED_EMPTY, S_FULL, P_FULL, DP_FULL, DS_FULL, ACC_FULL, ACC_EMPTY, ROW_FULL, ROW_READ = ROW_FULL + 2,
          FULL = ROW_READ + 2, EMPTY = FULL + STAGES, DRAIN = EMPTY + STAGES, NBAR };
@@ -217,19 +313,36 @@ __device__ __forceinline__ void keys_body(const Args& a, unsigned char* smem, in
     counts[i] = (i == P_FULL || i == DS_FULL || i == ACC_EMPTY || i == ROW_READ || i == ROW_READ + 1) ? EW_WARPS : 1;
   Block k;
   if (!start<D>(smem, NBAR, counts, a.status, k)) return;
+  const int ksplits = deal.ksplits, kper = deal.kper, kitems = deal.kitems;
   auto bar = [&](int i) { return k.bar0 + 8u * (uint32_t)i; };
   auto stage = [&](uint32_t i) { return k.base + (2u + i % STAGES) * L::BYTES; };
   const int L_all = a.G * a.qtiles;          // query tiles of a key head
-  // item: key tile kt of (b, hk), query tiles [t0, t0 + tiles)
-  auto item = [&](int it, int valid, int& b, int& hk, int& kt, int& t0) -> int {
-    const int split = it % a.ksplits, u = it / a.ksplits;
-    kt = u % a.ktiles;
-    hk = u / a.ktiles % a.Hkv;
-    b = u / a.ktiles / a.Hkv;
-    t0 = split * a.kper;
-    return kt * TILE < valid ? max(0, min(a.kper, L_all - t0)) : 0;
+  // query tiles of item it: none where the key tile has no kept key (dealt items have)
+  auto share = [&](int it) -> int {
+    if (!a.dealt && a.key_len != nullptr) {
+      const int u = it / ksplits;
+      if (u % a.ktiles * TILE >= item_len(a.key_len, a.Nk, u / (a.ktiles * a.Hkv), nullptr, false)) return 0;
+    }
+    return min(kper, L_all - it % ksplits * kper);
   };
-  auto kept = [&](int it) { return item_len(a.key_len, a.Nk, it / (a.ksplits * a.ktiles * a.Hkv), nullptr, false); };
+  // item it: key tile kt of (b, hk), from query tile t0 on; b and the key tiles a head before it go on with it
+  struct Walk { int b, before, count; };
+  auto tiles_of = [&](int b) { return (item_len(a.key_len, a.Nk, b, nullptr, false) + TILE - 1) / TILE; };
+  auto next = [&](Walk& w, int it, int& hk, int& kt, int& t0) {
+    const int u = it / ksplits;
+    if (!a.dealt) {
+      w.b = u / (a.Hkv * a.ktiles);
+      w.before = w.b * a.ktiles;
+    } else {
+      while (u >= a.Hkv * (w.before + w.count) && w.b + 1 < a.B) {
+        w.before += w.count;
+        w.count = tiles_of(++w.b);
+      }
+    }
+    hk = (u - a.Hkv * w.before) / w.count;
+    kt = (u - a.Hkv * w.before) % w.count;
+    t0 = it % ksplits * kper;
+  };
 
   if (k.warp < EW_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -249,9 +362,8 @@ __device__ __forceinline__ void keys_body(const Args& a, unsigned char* smem, in
       __syncwarp();
       if (k.lane == 0) mbar_arrive(bar(i));
     };
-    for (int it = block; ok && it < a.kitems; it += blocks) {
-      int b, hk, kt, t0;
-      const int tiles = item(it, kept(it), b, hk, kt, t0);
+    for (int it = block; ok && it < kitems; it += blocks) {
+      const int tiles = share(it);
       if (tiles == 0) continue;
       for (int j = 0; j < tiles; ++j, ++nt) {
         // lse log2 e and D of the tile's queries: one value per column, read by all lanes at once
@@ -317,10 +429,13 @@ __device__ __forceinline__ void keys_body(const Args& a, unsigned char* smem, in
     if (k.lane == 0) {
       uint32_t nf = 0, nk = 0, nr = 0;
       bool ok = true;
-      for (int it = block; ok && it < a.kitems; it += blocks) {
-        int b, hk, kt, t0;
-        const int tiles = item(it, kept(it), b, hk, kt, t0);
+      Walk w = a.dealt ? Walk{deal.b, deal.before, tiles_of(deal.b)} : Walk{0, 0, a.ktiles};
+      for (int it = block; ok && it < kitems; it += blocks) {
+        const int tiles = share(it);
         if (tiles == 0) continue;
+        int hk, kt, t0;
+        next(w, it, hk, kt, t0);
+        const int b = w.b;
         if (nf > 0) ok = mbar_wait(bar(FIXED_EMPTY), (nf - 1) & 1u, a.status);
         if (!ok || *k.abort_flag) { ok = false; break; }
         mbar_arrive_tx(bar(FIXED_FULL), 2 * L::BYTES);
@@ -364,9 +479,8 @@ __device__ __forceinline__ void keys_body(const Args& a, unsigned char* smem, in
     };
     auto wait_stage = [&](uint32_t i) { return wait(FULL + i % STAGES, (i / STAGES) & 1u); };
     const uint32_t sK = k.base, sV = k.base + L::BYTES;
-    for (int it = block; ok && it < a.kitems; it += blocks) {
-      int b, hk, kt, t0;
-      const int tiles = item(it, __shfl_sync(0xffffffffu, kept(it), 0), b, hk, kt, t0);
+    for (int it = block; ok && it < kitems; it += blocks) {
+      const int tiles = __shfl_sync(0xffffffffu, share(it), 0);
       if (tiles == 0) continue;
       if (!wait(FIXED_FULL, ni & 1u) || !wait_stage(nk)) break;
       product_nt<D>(e, k.tmem, sK, stage(nk), TILE);
@@ -425,7 +539,7 @@ __device__ __forceinline__ void keys_body(const Args& a, unsigned char* smem, in
 // One TMA warp brings Q and dO (the next dO, which has to wait for its buffer, is
 // asked into L2 meanwhile), one K and V. Four warps write dQ out.
 template <int D, bool STAY>
-__device__ __forceinline__ void rows_body(const Args& a, unsigned char* smem, int block, int blocks) {
+__device__ __forceinline__ void rows_body(const Args& a, const Deal& deal, unsigned char* smem) {
   using L = Lay<D>;
   constexpr int ROW_TMA_WARP = 10;
   enum { Q_FULL = 0, Q_READ = 3, DS_FULL = 6, DO_FULL = 8, DO_READ, V_FULL, V_READ, S_FULL, S_READ, DP_FULL, DP_READ,
@@ -445,9 +559,7 @@ __device__ __forceinline__ void rows_body(const Args& a, unsigned char* smem, in
   // K of tile t of all, tile j of its item
   auto k_at = [&](uint32_t t, int j) { return STAY ? (uint32_t)j : t % NK; };
   auto sK = [&](uint32_t i) { return sV + (1u + i) * L::BYTES; };
-  // this CTA's items: every blocks-th, or q_per in a row
-  const int it0 = a.q_per ? block * a.q_per : block, step = a.q_per ? 1 : blocks;
-  const int end = a.q_per ? min(it0 + a.q_per, a.qitems) : a.qitems;
+  const int it0 = deal.first, step = deal.step, end = deal.end;
   // item: query tile qt of (b, h), key tiles [k0, k0 + tiles)
   auto item = [&](int it, int valid, int& b, int& h, int& qt, int& k0) -> int {
     const int split = it % a.qsplits, u = it / a.qsplits;
@@ -731,11 +843,25 @@ __device__ __forceinline__ void rows_body(const Args& a, unsigned char* smem, in
 }
 
 // Blocks of dQ first, then of dK and dV: those begin as the first ones end.
-template <int D, bool STAY>
+template <int D>
 __global__ void __launch_bounds__(THREADS, 1) main_kernel(const __grid_constant__ Args a, int row_blocks) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  if ((int)blockIdx.x < row_blocks) rows_body<D, STAY>(a, smem, blockIdx.x, row_blocks);
-  else keys_body<D>(a, smem, blockIdx.x - row_blocks, gridDim.x - row_blocks);
+  const bool rows = (int)blockIdx.x < row_blocks;
+  const int block = rows ? blockIdx.x : blockIdx.x - row_blocks, blocks = rows ? row_blocks : gridDim.x - row_blocks;
+  Deal deal;
+  if (a.dealt) {
+    Deal* dealt = reinterpret_cast<Deal*>(smem + Lay<D>::OFF_DEAL);
+    wait_for_last();
+    if (threadIdx.x < 32) deal_out(a, rows, block, blocks, dealt);
+    __syncthreads();
+    deal = *dealt;
+  } else {
+    const int per = (a.qitems + blocks - 1) / blocks;
+    deal = Deal{a.ksplits, a.kper, a.kitems, 0, 0, block * per, min((block + 1) * per, a.qitems), 1, a.ktiles <= 2 && a.qsplits == 1};
+  }
+  if (!rows) keys_body<D>(a, deal, smem, block, blocks);
+  else if (deal.stay) rows_body<D, true>(a, deal, smem);
+  else rows_body<D, false>(a, deal, smem);
 }
 
 // ------------------------------------------------------------------ shares
@@ -749,14 +875,17 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ Args a
   const int n = blockIdx.x * (1024 / D) + x / (D / 8), c = 8 * (x % (D / 8));
   if (n >= a.Nk) return;
   int row = a.place ? a.place[(size_t)b * a.Nk + n] : n;
-  if (row >= item_len(a.key_len, a.Nk, b, nullptr, false)) row = -1;
+  const int len = item_len(a.key_len, a.Nk, b, nullptr, false);
+  if (row >= len) row = -1;
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
   if (row >= 0) {
-    const size_t it = (((size_t)b * a.Hkv + hk) * a.ktiles + row / TILE) * a.ksplits;
+    const int before = a.dealt ? a.deal[4 + b] : b * a.ktiles, tiles = a.dealt ? (len + TILE - 1) / TILE : a.ktiles;
+    const int splits = a.dealt ? a.deal[0] : a.ksplits;
+    const size_t it = ((size_t)a.Hkv * before + (size_t)hk * tiles + row / TILE) * splits;
 #pragma unroll 4
-    for (int s = 0; s < a.ksplits; ++s) {
+    for (int s = 0; s < splits; ++s) {
       const float4* src = reinterpret_cast<const float4*>(a.part + (((it + s) * 2 + y) * TILE + row % TILE) * D + c);
       const float4 u = src[0], w = src[1];
       v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
@@ -789,55 +918,44 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const __grid_constant__ A
 }
 
 struct Plan {
-  size_t off_lse, off_delta, off_part, off_qpart, bytes;
+  size_t off_lse, off_delta, off_deal, off_part, off_qpart, bytes;
+  int kslots;                                // shares of dK and dV there is room for
 };
 
-// even: every item keeps all its keys.
-static Plan plan(const Problem& p, bool even, Args* a) {
+static Plan plan(const Problem& p, Args* a) {
   a->B = p.B; a->Hq = p.Hq; a->Hkv = p.Hkv; a->G = p.G; a->Nq = p.Nq; a->Nk = p.Nk;
   a->qtiles = (p.Nq + TILE - 1) / TILE;
   a->ktiles = (p.Nk + TILE - 1) / TILE;
   a->NqP = a->qtiles * TILE;
-  // shares of a key tile's queries: the fewest of those within 2% of the least
-  // time, in tiles: the rounds of items times the tiles of an item and four more (its
-  // 128 KB of sums, written and read again, take about that long); with lengths
-  // that differ, about 0.6 of the work on average and one item for what it is uneven
-  const int64_t units = (int64_t)p.B * p.Hkv * a->ktiles;
-  const int64_t L = (int64_t)p.G * a->qtiles;
-  auto cost = [&](int64_t s) {
-    const double item = (double)((L + s - 1) / s + 4);
-    return item * (even ? (double)((units * s + SM_COUNT - 1) / SM_COUNT) : 0.6 * units * s / SM_COUNT + 1.0);
-  };
-  const int64_t most = std::min<int64_t>(L, std::max<int64_t>(1, 12 * SM_COUNT / std::max<int64_t>(units, 12)));
-  double least = cost(1);
-  for (int64_t s = 2; s <= most; ++s) least = std::min(least, cost(s));
-  int64_t ks = 1;
-  while (cost(ks) > least * 1.02) ++ks;
-  a->kper = (int)((L + ks - 1) / ks);
-  a->ksplits = (int)((L + a->kper - 1) / a->kper);
-  a->kitems = (int)(units * a->ksplits);
+  const int units = p.B * p.Hkv * a->ktiles, L = p.G * a->qtiles, most = most_shares(units, L);
+  float least = share_cost(units, L, 1);
+  for (int x = 2; x <= most; ++x) least = std::min(least, share_cost(units, L, x));
+  int ks = 1;
+  while (share_cost(units, L, ks) > least * 1.02f) ++ks;
+  a->kper = (L + ks - 1) / ks;
+  a->ksplits = (L + a->kper - 1) / a->kper;
+  a->kitems = units * a->ksplits;
   const int64_t rows = (int64_t)p.B * p.Hq * a->qtiles;
   a->qsplits = (int)std::max<int64_t>(1, std::min<int64_t>(a->ktiles, SM_COUNT / rows));
   a->qitems = (int)(rows * a->qsplits);
-  a->stay = a->ktiles <= 2 && a->qsplits == 1;
-  // lengths differ between items: spread them
-  a->q_per = even ? (a->qitems + SM_COUNT - 1) / SM_COUNT : 0;
   Plan pl;
   size_t o = 0;
   auto take = [&](size_t n) { const size_t at = o; o = align_up(o + n); return at; };
   pl.off_lse = take((size_t)p.B * p.Hq * a->NqP * 4);
   pl.off_delta = take((size_t)p.B * p.Hq * a->NqP * 4);
-  pl.off_part = take((size_t)a->kitems * 2 * TILE * p.d * 4);
+  // (with lengths the kernel chooses the shares: as many as there may be)
+  pl.kslots = (int)std::min<int64_t>(std::max(units, KSLOTS), (int64_t)units * L);
+  pl.off_deal = take((4 + (size_t)p.B) * 4);
+  pl.off_part = take((size_t)pl.kslots * 2 * TILE * p.d * 4);
   pl.off_qpart = take(a->qsplits > 1 ? (size_t)a->qitems * TILE * p.d * 4 : 0);
   pl.bytes = o;
   return pl;
 }
 
 template <int D>
-static cudaError_t run(const Args& a, const PackArgs& pack, cudaStream_t s) {
-  const auto main = a.stay ? main_kernel<D, true> : main_kernel<D, false>;
-  static std::atomic<uint64_t> done[2] = {};
-  const cudaError_t e = allow_shared(main, Lay<D>::SMEM, &done[a.stay ? 1 : 0]);
+static cudaError_t run(const Args& a, int key_blocks, const PackArgs& pack, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(main_kernel<D>, Lay<D>::SMEM, &done);
   if (e != cudaSuccess) return e;
   const int row_blocks = std::min(a.qitems, SM_COUNT);
   const int per_head = (a.NqP * (D / 64) + 127) / 128;
@@ -846,7 +964,7 @@ static cudaError_t run(const Args& a, const PackArgs& pack, cudaStream_t s) {
   stat_kernel<D><<<(unsigned)all, 256, 0, s>>>(a, pack, per_head, (int)stat_blocks);
   cudaError_t l = cudaGetLastError();
   if (l == cudaSuccess)
-    l = launch_behind(main, dim3(row_blocks + std::min(a.kitems, SM_COUNT)), THREADS, Lay<D>::SMEM, s, a, row_blocks);
+    l = launch_behind(main_kernel<D>, dim3(row_blocks + key_blocks), THREADS, Lay<D>::SMEM, s, a, row_blocks);
   if (l == cudaSuccess) l = launch_behind(sum_kernel<D>, dim3((a.Nk * (D / 64) + 15) / 16, a.Hkv, a.B), 256, 0, s, a);
   if (l == cudaSuccess && a.qsplits > 1)
     l = launch_behind(sum_rows_kernel<D>, dim3((a.Nq * (D / 64) + 15) / 16, a.B * a.Hq), 256, 0, s, a);
@@ -855,15 +973,14 @@ static cudaError_t run(const Args& a, const PackArgs& pack, cudaStream_t s) {
 
 }  // namespace bwd
 
-// The size does not depend on a call's masks: room for either plan.
 size_t bwd_workspace(const Problem& p) {
   bwd::Args a = {};
-  return std::max(bwd::plan(p, true, &a).bytes, bwd::plan(p, false, &a).bytes);
+  return bwd::plan(p, &a).bytes;
 }
 
 cudaError_t launch_bwd(const Problem& p, const Gradients& g, const PackArgs& pack, void* ws, cudaStream_t s) {
   bwd::Args a = {};
-  const bwd::Plan pl = bwd::plan(p, p.key_len == nullptr, &a);
+  const bwd::Plan pl = bwd::plan(p, &a);
   if (!make_tensor_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, false, bwd::TILE) ||
       !make_tensor_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
       !make_tensor_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, false, bwd::TILE) ||
@@ -880,9 +997,12 @@ cudaError_t launch_bwd(const Problem& p, const Gradients& g, const PackArgs& pac
   a.sl2 = p.scale * 1.4426950408889634f;
   a.lse2 = reinterpret_cast<float*>(w + pl.off_lse);
   a.delta = reinterpret_cast<float*>(w + pl.off_delta);
+  a.deal = reinterpret_cast<int*>(w + pl.off_deal);
   a.part = reinterpret_cast<float*>(w + pl.off_part);
   a.qpart = reinterpret_cast<float*>(w + pl.off_qpart);
-  return p.d == 128 ? bwd::run<128>(a, pack, s) : bwd::run<64>(a, pack, s);
+  a.dealt = p.key_len != nullptr && (a.qitems > SM_COUNT || a.kitems > SM_COUNT);
+  const int key_blocks = std::min(a.dealt ? pl.kslots : a.kitems, SM_COUNT);
+  return p.d == 128 ? bwd::run<128>(a, key_blocks, pack, s) : bwd::run<64>(a, key_blocks, pack, s);
 }
 
 }  // namespace cross

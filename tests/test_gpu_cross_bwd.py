@@ -114,3 +114,31 @@ def test_cross_gradient_captured_beside_an_eager_call():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, other, here))
     assert spark.get_status() == 0
+
+
+# lengths of many items and many tiles: key tiles and query tiles are shared out on the device
+@pytest.mark.parametrize("c", [
+    (40, 4, 2, 130, 300, 64, "bf16", "lengths mask"),
+    (70, 2, 2, 200, 130, 128, "bf16", "lengths"),
+    (3, 20, 20, 500, 300, 128, "bf16", "empty"),
+    (2, 16, 16, 700, 600, 128, "bf16", "lengths"),
+    (2, 12, 4, 1200, 700, 64, "bf16", "mask"),
+    (3, 4, 1, 40, 9000, 64, "bf16", "lengths"),
+], ids=ids)
+def test_cross_gradient_shared_out(c):
+    test_cross_gradient(c)
+
+
+@pytest.mark.parametrize("lengths", [(0, 0, 0, 0), (0, 600, 0, 3), (256, 1, 128, 129), (600, 600, 600, 600)])
+def test_cross_gradient_of_given_lengths(lengths):
+    p, q, k, v, _ = inputs(4, 16, 8, 700, 600, 64)
+    kw = {"key_len": torch.tensor(lengths, dtype=torch.int32, device="cuda")}
+    dout, out, lse, grads = gradient(p, q, k, v, kw)
+    assert spark.get_status() == 0
+    wants, bounds = o64.Cross(q, k, v, **kw).backward(dout)
+    for got, want, bound, name in zip(grads, wants, bounds, ("dq", "dk", "dv")):
+        o64.check(got, want, bound, name)
+    for b, n in enumerate(lengths):
+        assert (grads[1][b, :, n:] == 0).all() and (grads[2][b, :, n:] == 0).all()
+        if n == 0:
+            assert (grads[0][b] == 0).all()
