@@ -423,7 +423,8 @@ typedef struct {
  *   ws           : workspace of spark_cross_workspace_size(p, 0) bytes (scratch;
  *                  calls that may overlap need one each)
  * P is rounded to the tensors' type for P V, sums and statistics are float32.
- * One launch, two with a mask or where the keys are split over blocks. */
+ * One launch; another before it with a mask and many rows, another behind it
+ * where the keys are split over blocks that do not join among themselves. */
 size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd);
 spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, const spark_view* k,
                               const spark_view* v, const int32_t* key_len, const uint8_t* key_mask,
