@@ -19,10 +19,11 @@
 // registers (four blocks an SM) reads and writes 72,576 tokens of 80 heads
 // (bf16, d = 128) in 461 us = 6.4 TB/s, with 80 registers in 510; a software
 // pipeline of the loads (more in flight a thread, fewer warps) took 508 to 750.
-// Heads a block: for at least six blocks an SM in all (24: the angles are
-// formed for four heads at a time, 41 against 32 us at 7,110 tokens of 32 heads;
-// the gradient's blocks with partial sums, 888: 87 us, 444: 88, 2,664: 90).
-// 16-bit values are converted in pairs: value by value those took 31 us, now 29.
+// Heads a block: as many as leave three blocks an SM in all (2 x 3,555 tokens of
+// 24 + 8 heads, fp16: 26.4 us; for six blocks 29.1, for 24, where the angles are
+// formed for four heads at a time, 41; 3 x 1,517 tokens of 24 heads 11.0 against
+// 14.5 for six). The gradient's blocks with partial sums, 888: 87 us, 444: 88, 2,664: 90.
+// 16-bit values are converted in pairs: value by value those took 31 us, in pairs 29.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -462,7 +463,7 @@ static Args plan(const spark_rotary_params* p, const float* pos) {
   // SM a few blocks
   const int tok = THREADS / (p->d / 8);
   a.tiles = (p->N + tok - 1) / tok;
-  const int64_t tiles = (int64_t)a.tiles * p->B, want = SM_COUNT * 6;
+  const int64_t tiles = (int64_t)a.tiles * p->B, want = SM_COUNT * 3;
   const int heads = p->Hq + p->Hk;
   const int64_t share = std::max<int64_t>(1, tiles * heads / want);      // heads a block, for `want` blocks in all
   for (int x = 0; x < 2; ++x) {
