@@ -28,7 +28,7 @@ cudaError_t launch_few(const Problem& p, void* ws, cudaStream_t s);
 // key_len[b] of an item; key_mask is not looked at.
 size_t many_workspace(const Problem& p);
 void many_keys(const Problem& p, int64_t* keys, int* shares);   // keys of a CTA's items, shares of a row tile
-cudaError_t launch_many(const Problem& p, void* ws, cudaStream_t s);
+cudaError_t launch_many(const Problem& p, bool packed, void* ws, cudaStream_t s);   // packed: launch_pack came just before
 
 // The kept keys of each item moved to the front: k and v become contiguous
 // [B,Hkv,Nk,d] copies in ws whose first count[b] rows are the kept ones in

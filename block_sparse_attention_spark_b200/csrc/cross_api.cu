@@ -108,7 +108,7 @@ spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, 
   if (few) return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
   const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + own);
   if (packed.mask != nullptr && cross::launch_pack(packed, stream) != cudaSuccess) return SPARK_ERR_CUDA;
-  return cross::launch_many(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  return cross::launch_many(c, packed.mask != nullptr, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
 spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view* q, const spark_view* k,

@@ -584,11 +584,18 @@ static size_t workspace(const Problem& p, const Args& a) {
 }
 
 template <int D, bool H>
-static cudaError_t run(const Args& a, cudaStream_t s) {
+static cudaError_t run(const Args& a, bool packed, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(kernel<D, H>, Lay<D>::SMEM, &done);
   if (e != cudaSuccess) return e;
-  const cudaError_t l = launch_behind(kernel<D, H>, dim3(std::min(a.items, SM_COUNT)), THREADS, Lay<D>::SMEM, s, a);
+  const int blocks = std::min(a.items, SM_COUNT);
+  cudaError_t l;
+  if (packed) {                              // behind this call's packing; else what came before is not known
+    l = launch_behind(kernel<D, H>, dim3(blocks), THREADS, Lay<D>::SMEM, s, a);
+  } else {
+    kernel<D, H><<<blocks, THREADS, Lay<D>::SMEM, s>>>(a);
+    l = cudaGetLastError();
+  }
   if (l != cudaSuccess || a.splits == 1) return l;
   const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
   if (a.splits > 32 || (a.splits > 4 && rows <= 8 * SM_COUNT)) 
@@ -612,7 +619,7 @@ void many_keys(const Problem& p, int64_t* keys, int* shares) {
   *shares = a.splits;
 }
 
-cudaError_t launch_many(const Problem& p, void* ws, cudaStream_t s) {
+cudaError_t launch_many(const Problem& p, bool packed, void* ws, cudaStream_t s) {
   many::Args a = {};
   many::plan(p, &a);
   if (!make_tensor_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, p.fp16, many::ROWS) ||
@@ -627,8 +634,8 @@ cudaError_t launch_many(const Problem& p, void* ws, cudaStream_t s) {
   a.wide = ((uintptr_t)p.out.data % 32 == 0 && p.out.b % 16 == 0 && p.out.h % 16 == 0 && p.out.n % 16 == 0);
   a.part = static_cast<float*>(ws);
   a.stat = reinterpret_cast<float2*>(a.part + (size_t)a.items * many::SLOTS * many::ROWS * p.d);
-  if (p.d == 128) return p.fp16 ? many::run<128, true>(a, s) : many::run<128, false>(a, s);
-  return p.fp16 ? many::run<64, true>(a, s) : many::run<64, false>(a, s);
+  if (p.d == 128) return p.fp16 ? many::run<128, true>(a, packed, s) : many::run<128, false>(a, packed, s);
+  return p.fp16 ? many::run<64, true>(a, packed, s) : many::run<64, false>(a, packed, s);
 }
 
 }  // namespace cross

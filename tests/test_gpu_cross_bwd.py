@@ -142,3 +142,31 @@ def test_cross_gradient_of_given_lengths(lengths):
         assert (grads[1][b, :, n:] == 0).all() and (grads[2][b, :, n:] == 0).all()
         if n == 0:
             assert (grads[0][b] == 0).all()
+
+
+def test_cross_attention_and_gradient_in_a_forked_capture():
+    """Two branches of one captured graph, each with a workspace of its own, behind copies and joined again."""
+    p, q, k, v, kw = inputs(2, 20, 20, 300, 200, 64, mask="lengths mask")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    dout = rand(g, q.shape, q.dtype)
+    want, lse = spark.cross_attn(p, q, k, v, return_lse=True, **kw)
+    grads = spark.cross_attn_bwd(p, q, k, v, want, lse, dout, **kw)
+    plain = spark.cross_attn(p, q, k, v)
+    x, other = torch.zeros_like(q), torch.cuda.Stream()
+    ws = [spark.alloc_cross_workspace(p, bwd=b) for b in (False, False, True)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.copy_(q)
+        main = torch.cuda.current_stream()
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            a = spark.cross_attn(p, x, k, v, ws=ws[0])
+        b, l = spark.cross_attn(p, x, k, v, ws=ws[1], return_lse=True, **kw)
+        main.wait_stream(other)
+        c = spark.cross_attn_bwd(p, x, k, v, b, l, dout, ws=ws[2], **kw)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, plain) and torch.equal(b, want) and torch.equal(l, lse)
+    assert all(torch.equal(s, t) for s, t in zip(c, grads))
+    assert spark.get_status() == 0
