@@ -60,6 +60,12 @@ cudaError_t launch_bwd(const Problem& p, const Gradients& g, const PackArgs& pac
 
 inline size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// The kernels' workspace begins at the first multiple of 256 bytes in the caller's,
+// which is only 16-byte aligned: partial sums are written in 32-byte stores. The
+// sizes callers are told have WS_SLACK for that.
+constexpr size_t WS_SLACK = 256;
+inline char* workspace_base(void* ws) { return reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(ws))); }
+
 #ifdef __CUDACC__
 }  // namespace cross
 }  // namespace spark

@@ -54,7 +54,7 @@ static bool few_rows(const Problem& c) {
 // size covers calls with and without a mask).
 static size_t forward_bytes(const Problem& c, bool few) { return few ? few_workspace(c) : align_up(many_workspace(c)); }
 static size_t backward_bytes(const Problem& c) { return align_up(bwd_workspace(c)); }
-static size_t total_bytes(const Problem& c, size_t own, bool packs) { return own + (packs ? pack_plan(c).bytes : 0) + 256; }
+static size_t total_bytes(const Problem& c, size_t own, bool packs) { return own + (packs ? pack_plan(c).bytes : 0) + WS_SLACK; }
 
 // What packing a masked problem's keys into ws takes; the problem is then the packed one.
 static PackArgs pack(Problem* c, char* ws) {
@@ -105,10 +105,11 @@ spark_status spark_cross_attn(const spark_cross_params* p, const spark_view* q, 
   c.key_mask = key_mask;
   c.lse = lse;
   c.status = device_status();
-  if (few) return cross::launch_few(c, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
-  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + own);
+  char* base = cross::workspace_base(ws);
+  if (few) return cross::launch_few(c, base, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  const cross::PackArgs packed = cross::pack(&c, base + own);
   if (packed.mask != nullptr && cross::launch_pack(packed, stream) != cudaSuccess) return SPARK_ERR_CUDA;
-  return cross::launch_many(c, packed.mask != nullptr, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  return cross::launch_many(c, packed.mask != nullptr, base, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
 spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view* q, const spark_view* k,
@@ -135,8 +136,9 @@ spark_status spark_cross_attn_bwd(const spark_cross_params* p, const spark_view*
   c.key_len = key_len;
   c.key_mask = key_mask;
   c.status = device_status();
-  const cross::PackArgs packed = cross::pack(&c, static_cast<char*>(ws) + own);
-  return cross::launch_bwd(c, g, packed, ws, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
+  char* base = cross::workspace_base(ws);
+  const cross::PackArgs packed = cross::pack(&c, base + own);
+  return cross::launch_bwd(c, g, packed, base, stream) == cudaSuccess ? SPARK_OK : SPARK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -324,7 +324,8 @@ size_t spark_workspace_region(const spark_params* p, int32_t region, size_t* byt
  * pointers are on the current device. An output overlaps no input unless the call
  * says so. d is 64 or 128. Everything else is as for the calls above: asynchronous
  * on the stream, no allocation, no fallback, and calls whose kernels may overlap
- * (other streams, graphs replayed at the same time) need a workspace each.
+ * (other streams, graphs replayed at the same time) need a workspace each. A
+ * workspace is 16-byte aligned (SPARK_ERR_INVALID_ARG otherwise).
  * Inputs are finite except where a call says that they are not looked at.
  * Make the first call on a device outside of a stream capture.
  * Sizes below 1 are SPARK_ERR_INVALID_ARG (masks may still leave no key). */
