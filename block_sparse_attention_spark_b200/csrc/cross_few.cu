@@ -26,6 +26,10 @@ constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int ROWS = 16, KEYS = 32, STAGES = 3;
 constexpr int MIN_KEYS = WARPS * KEYS;       // fewest keys worth a block of their own
 constexpr int CLUSTER = 8;                   // most blocks of a tile that join among themselves
+// Weights are 2^(logit - maximum + ABOVE): fp16 ends at 2^16 and loses what is below
+// 2^-25, so that weights down to 2^-40 of the row's largest count in P V as they do
+// in the sum. Statistics hold maximum - ABOVE, what the weights are relative to.
+template <bool H> constexpr float ABOVE = H ? 15.0f : 0.0f;
 
 struct Args {
   Problem p;
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
       }
     }
     // (logits all -inf so far: exp2(-inf - 0) = 0; NaN stays NaN and reaches sum and O)
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - ABOVE<H>, m[1] == -INFINITY ? 0.f : m[1] - ABOVE<H>};
 #pragma unroll
     for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
@@ -251,8 +255,8 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
     if (r0 + 8 < live) *reinterpret_cast<float2*>(so + ((warp * ROWS + r0 + 8) * D + c)) = make_float2(o[n][2], o[n][3]);
   }
   if ((lane & 3) == 0) {
-    ss[warp * ROWS + r0] = make_float2(m[0], l[0]);
-    ss[warp * ROWS + r0 + 8] = make_float2(m[1], l[1]);
+    ss[warp * ROWS + r0] = make_float2(m[0] - ABOVE<H>, l[0]);
+    ss[warp * ROWS + r0 + 8] = make_float2(m[1] - ABOVE<H>, l[1]);
   }
   __syncthreads();
   float* wf = so + WARPS * ROWS * D + 2 * WARPS * ROWS;                 // [WARPS][ROWS] weights of the join

@@ -19,9 +19,9 @@
 // next item, whose Q (a third buffer) and K are already there.
 //
 // The softmax is online with a lazy reference: the row's reference maximum
-// moves (and O is rescaled in TMEM) only when a logit passes it by 2^8. Sums
-// and maxima are float32; P is rounded to the tensors' type, the operand type
-// of the MMA. The last tile of an item runs with N (and for P V, K) cut to the
+// moves (and O is rescaled in TMEM) only when a logit passes it by 8 (fp16: 6)
+// in powers of two. Sums and maxima are float32; P is rounded to the tensors'
+// type, the operand type of the MMA. The last tile of an item runs with N (and for P V, K) cut to the
 // next multiple of 16 of its keys; V rows between are zeroed in shared memory,
 // whatever they hold, because 0 * NaN is NaN.
 //
@@ -56,7 +56,12 @@ constexpr int THREADS = 32 * (SM_WARPS + 8);
 constexpr int LAUNCH_REGS = 128, SOFTMAX_REGS = 184, OTHER_REGS = 72;
 static_assert(SM_WARPS * 32 * SOFTMAX_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS, "registers the block owns");
 constexpr int QBUFS = 3;                     // a row tile's Q can load while both current ones are in use
-constexpr float LAZY = 8.0f;                 // log2 units
+// Log2 units: how far a logit passes the largest one that the reference was taken
+// from before the reference moves, and how far the reference lies below that one.
+// fp16 ends at 2^16 and loses what is below 2^-25, so its weights are formed up to
+// 2^15: those down to 2^-34 of the row's largest count in P V as they do in the sum.
+template <bool H> constexpr float LAZY = H ? 6.0f : 8.0f;
+template <bool H> constexpr float BELOW = H ? 9.0f : 0.0f;
 constexpr uint32_t O_COL = 256;
 
 struct Args {
@@ -190,11 +195,11 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         auto move = [&](float mt) {
           float corr = 1.f;
           if (m == -INFINITY) {
-            m = mt;
-          } else if (mt > m + LAZY) {
-            corr = ex2(m - mt);
+            m = mt - BELOW<H>;
+          } else if (mt > m + (BELOW<H> + LAZY<H>)) {
+            corr = ex2(m - (mt - BELOW<H>));
             l *= corr;
-            m = mt;
+            m = mt - BELOW<H>;
           }
           if (__any_sync(0xffffffffu, corr != 1.f)) {
             // P_{j-1} V_{j-1} is done (S_j came after it), P_j V_j not issued yet

@@ -423,7 +423,8 @@ typedef struct {
  *   lse          : [B,Hq,Nq] float32 device or NULL
  *   ws           : workspace of spark_cross_workspace_size(p, 0) bytes (scratch;
  *                  calls that may overlap need one each)
- * P is rounded to the tensors' type for P V, sums and statistics are float32.
+ * P is rounded to the tensors' type for P V (fp16: weights below 2^-34 of the
+ * row's largest are zero there), sums and statistics are float32.
  * One launch; another before it with a mask and many rows, another behind it
  * where the keys are split over blocks that do not join among themselves. */
 size_t spark_cross_workspace_size(const spark_cross_params* p, int32_t bwd);
