@@ -80,6 +80,16 @@ __device__ __forceinline__ int item_len(const int32_t* key_len, int Nk, int b, i
   if (report) set_status(status, STATUS_BAD_INPUT);
   return n < 0 ? 0 : Nk;
 }
+// A value of the result before it is rounded. The weights of P V are rounded, those
+// of the sum are not, so values near fp16's largest (65,504) may come out up to
+// 2^-11 past it, where rounding would make them infinite.
+template <bool H>
+__device__ __forceinline__ float in_range(float x) {
+  if constexpr (H) {
+    if (fabsf(x) < 65568.f) x = fminf(fmaxf(x, -65504.f), 65504.f);
+  }
+  return x;
+}
 #endif
 
 }  // namespace cross

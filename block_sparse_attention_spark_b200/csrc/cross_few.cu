@@ -88,7 +88,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 template <bool H>
 __device__ __forceinline__ void put4(char* dst, const float4& v) {
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack<H>(v.x, v.y), pack<H>(v.z, v.w));
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack<H>(in_range<H>(v.x), in_range<H>(v.y)),
+                                            pack<H>(in_range<H>(v.z), in_range<H>(v.w)));
 }
 // v += f * x
 __device__ __forceinline__ void add4(float4& v, float f, const float4& x) {

@@ -35,3 +35,39 @@ def test_many_small_weights_count(H, Nq, Nk, d, many):
     bound = 1000 * (share * (2 * 2.0 ** -11 + 64 * 27 * 2.0 ** -24) + Nk * 2.0 ** -34) + 2.0 ** -25
     assert (out.double() - 1000 * share).abs().max() <= bound
     assert (lse.double() - (logit - math.log1p(-share))).abs().max() <= 64 * 27 * 2.0 ** -24
+
+
+# the kernels as above; the last key's weight runs from half of the others' to 64 times theirs
+@pytest.mark.parametrize("H,Nq,Nk,d,many", [
+    (2000, 1, 5, 64, False), (40, 3, 700, 128, False), (1, 16, 40000, 64, False),
+    (160, 200, 5, 64, True), (100, 200, 130, 128, True), (1, 600, 20000, 64, True),
+])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_values_at_the_largest_of_the_type(H, Nq, Nk, d, many, sign):
+    """A mean of equal values is that value, the type's largest too: rounded weights do not carry it to infinity."""
+    p = spark.cross_params(1, H, Nq, Nk, d, heads_kv=1, dtype="fp16")
+    assert uses_tensor_cores(p) == many
+    n = H * Nq
+    q = torch.zeros(1, H, Nq, d, dtype=torch.float16, device="cuda")
+    q[..., 0] = torch.linspace(-1, 6, n, device="cuda").view(1, H, Nq)
+    k, v = (torch.zeros(1, 1, Nk, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    k[:, :, -1, 0] = math.log(2) * math.sqrt(d)
+    v[:] = sign * 65504.0
+    v[..., 1::2] = 1.0
+    out = spark.cross_attn(p, q, k, v)
+    assert spark.get_status() == 0
+    # weights off by 2^-11 each, and the rounding of the result
+    assert out.isfinite().all()
+    assert (out[..., ::2].double() - sign * 65504).abs().max() <= 65504 * 2 * 2.0 ** -11
+    assert (out[..., 1::2].double() - 1).abs().max() <= 2 * 2.0 ** -11
+
+
+def test_infinite_values_stay_infinite():
+    for H, Nq in ((2, 1), (160, 200)):
+        p = spark.cross_params(1, H, Nq, 70, 64, dtype="fp16")
+        g = torch.Generator(device="cuda").manual_seed(1)
+        q, k, v = (torch.randn(1, H, n, 64, generator=g, device="cuda").half() for n in (Nq, 70, 70))
+        v[:, :, 3, 5], v[:, :, 3, 6] = float("inf"), float("-inf")
+        out = spark.cross_attn(p, q, k, v)
+        assert torch.isposinf(out[..., 5]).all() and torch.isneginf(out[..., 6]).all()
+        assert out[..., 7:].isfinite().all()
