@@ -9,7 +9,9 @@ namespace cross {
 static spark_status validate(const spark_cross_params* p) {
   if (p == nullptr || p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->Nq < 1 || p->Nk < 1 || p->d < 1)
     return SPARK_ERR_INVALID_ARG;
-  if (p->Hq % p->Hkv != 0 || !isfinite(p->scale) || p->scale < 0.0) return SPARK_ERR_INVALID_ARG;
+  // (the kernels have scale log2 e in 32 bits)
+  if (p->Hq % p->Hkv != 0 || !isfinite((float)(p->scale * 1.4426950408889634)) || p->scale < 0.0)
+    return SPARK_ERR_INVALID_ARG;
   if (p->dtype < SPARK_BF16 || p->dtype > SPARK_FP32) return SPARK_ERR_INVALID_ARG;
   if (p->dtype == SPARK_FP32) return SPARK_ERR_UNSUPPORTED;
   if (p->d != 64 && p->d != 128) return SPARK_ERR_UNSUPPORTED;

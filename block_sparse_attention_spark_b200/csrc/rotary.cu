@@ -423,7 +423,7 @@ static spark_status validate(const spark_rotary_params* p) {
   if (p->axes < 1 || p->axes > 3) return SPARK_ERR_INVALID_ARG;
   if (p->pairing != SPARK_ROTARY_INTERLEAVED && p->pairing != SPARK_ROTARY_HALVES) return SPARK_ERR_INVALID_ARG;
   if (p->spectrum != SPARK_ROTARY_PER_AXIS && p->spectrum != SPARK_ROTARY_SHARED) return SPARK_ERR_INVALID_ARG;
-  if (!(p->theta > 0.0) || !isfinite(p->theta) || !(p->eps >= 0.0) || !isfinite(p->eps)) return SPARK_ERR_INVALID_ARG;
+  if (!(p->theta > 0.0) || !isfinite(p->theta) || !(p->eps >= 0.0) || !isfinite((float)p->eps)) return SPARK_ERR_INVALID_ARG;
   int64_t R = 0;
   for (int a = 0; a < p->axes; ++a) {
     if (p->dims[a] < 0 || p->dims[a] % 2 != 0) return SPARK_ERR_INVALID_ARG;

@@ -358,7 +358,7 @@ typedef struct {
                                   (last axis fastest, as for spark_positional_perm) */
   double theta;                /* > 0 */
   double start[3], scale[3];   /* angle = (start[a] + scale[a] * position) * frequency */
-  double eps;                  /* of the RMS norm, >= 0 */
+  double eps;                  /* of the RMS norm, >= 0, float32's range */
 } spark_rotary_params;
 
 /* Rotary positions of q and k, with the per-head RMS norm before them.
@@ -407,7 +407,7 @@ typedef struct {
   int32_t B, Hq, Hkv;          /* Hq a multiple of Hkv: query head h reads key head h / (Hq / Hkv) */
   int32_t Nq, Nk, d;           /* any lengths from 1 to SPARK_CROSS_MAX_TOKENS */
   int32_t dtype;               /* SPARK_BF16 | SPARK_FP16 (the gradient: SPARK_BF16) */
-  double scale;                /* of the logits; 0: 1/sqrt(d) */
+  double scale;                /* of the logits, >= 0, float32's range with log2 e; 0: 1/sqrt(d) */
 } spark_cross_params;
 
 /* Dense attention of Nq tokens over the Nk states of an encoder:
