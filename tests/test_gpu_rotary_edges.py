@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_sparse_attention_spark_b200 as spark
+from tests import operators64 as o64
 from tests.test_gpu_rotary import CASES, case, rand
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +51,19 @@ def test_rotary_gradient_in_place_of_rows_that_overflow(N):
     for _ in range(10):
         got = gradient_in_place(p, dy, None, q, None, w, None, None)
         assert torch.equal(got[0], dx) and torch.equal(got[2], want)
+
+
+@pytest.mark.parametrize("spectrum,dims,d", [("axis", (44, 42, 42), 128), ("shared", (16, 24, 24), 64)])
+def test_rotary_of_far_positions(spectrum, dims, d):
+    """Positions as far as float32 counts tokens, whole and fractional, on both sides of zero."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    B, H, N = 2, 2, 500
+    q = rand(g, (B, H, N, d), torch.float32)
+    pos = torch.randint(-2 ** 24, 2 ** 24, (B, N, 3), generator=g, device="cuda").float()
+    pos[:, ::3] = pos[:, ::3] / 64
+    p = spark.rotary_params(B, H, N, d, dims, heads_k=0, dtype="fp32", spectrum=spectrum)
+    ang = o64.angles(dims, spectrum, 10000.0, pos)
+    got, _ = spark.rotary(p, q, positions=pos)
+    want, bound = o64.rotary(q, None, ang, "interleaved", 0.0)
+    # both forms of a frequency are off by at most 2^-45 of it, and the far pairs turn slowly: below a step of 2^-24 each
+    o64.check(got, want, bound + 2 * 2.0 ** -24 * o64.pair_size(q.double(), sum(dims), "interleaved"), "q")
