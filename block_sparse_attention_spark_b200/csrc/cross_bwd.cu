@@ -6,23 +6,28 @@
 // Three launches: stat_kernel forms D and lse log2 e of the rows; main_kernel's
 // first blocks (rows_body, dQ) hold a tile of 128 queries and stream the keys, its
 // others (keys_body, dK and dV) hold a tile of 128 keys and stream the queries;
-// sum_kernel joins the shares of dK and dV. S and dP are formed twice, seven
-// products of 128x128x128 a tile pair where five would do: adding dQ up over key
-// tiles would take float32 atomics (Nk / 128 times Nq d of them, in an order
-// that changes) or one CTA for all the keys.
+// sum_kernel joins the shares of dK and dV. A fourth, sum_rows_kernel, where there
+// are so few query tiles that their keys are split too. S and dP are formed twice,
+// seven products of 128x128xd a tile pair where five would do: adding dQ up over
+// key tiles would take float32 atomics (Nk / 128 times Nq d of them, in an order
+// that changes) or one CTA for all the keys. (With one key tile there is nothing
+// to add up; a body for that case has not been built.)
 //
 // Both bodies: one persistent CTA per SM, eight warps on the elementwise part
 // (each thread one row of the tile's TMEM lanes and half of its 128 columns),
 // one warp on TMA, one on MMAs. P and dS are rounded to bf16, the operand type
 // of the MMA, in TMEM, where they are the A operand of the second product of
-// each chain. Products have N = 128 throughout (N = 64 runs at half the rate).
+// each chain. S and dP of whole tiles have N = 128 (in rows_body an item's last
+// key tile is cut to the next multiple of 16 keys), the second products N = d;
+// N = 64 runs at half the rate.
 // Sums, P before rounding and all statistics are float32.
 //
 // Measured (72,576 queries of 40 heads over 256 keys, d = 128): 1,520 us (1,713 in
-// a loop of 0.15 s): statistics 241 us = 6.2 TB/s, dQ about 600, dK and dV 620 =
-// 1.23 PFLOP/s of MMA work, 90% of what the card sustains in cuBLAS under its
-// 1,000 W (1.37): power bounds it (SM clock 1.52 GHz), exponentials on the FMA pipe
-// or fewer instructions in the elementwise warps changed nothing.
+// a loop of 0.15 s): statistics 241 us = 6.2 TB/s; dK and dV 620 = 1.23 PFLOP/s of
+// MMA work, 90% of what the card sustains in cuBLAS under its 1,000 W (1.37): power
+// bounds them (SM clock 1.52 GHz), exponentials on the FMA pipe or fewer
+// instructions in the elementwise warps changed nothing; dQ about 600 for three
+// products instead of four, 0.95: what keeps it below the others is not known.
 //
 // Bounded waits as in the forward kernels.
 #include "cross_pack.cuh"

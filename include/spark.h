@@ -328,7 +328,10 @@ size_t spark_workspace_region(const spark_params* p, int32_t region, size_t* byt
  * workspace is 16-byte aligned (SPARK_ERR_INVALID_ARG otherwise).
  * Inputs are finite except where a call says that they are not looked at.
  * Make the first call on a device outside of a stream capture.
- * Sizes below 1 are SPARK_ERR_INVALID_ARG (masks may still leave no key). */
+ * Sizes below 1 are SPARK_ERR_INVALID_ARG (masks may still leave no key). Limits
+ * (SPARK_ERR_UNSUPPORTED past them): lengths of SPARK_CROSS_MAX_TOKENS, 65,535
+ * heads in all (B (Hq + Hk) for rotary positions, B Hq for cross attention),
+ * 2^31 - 1 query rows B Hq Nq and key rows B Hkv Nk. */
 typedef struct {
   const void* data;
   int64_t b, h, n;             /* strides in elements */
@@ -459,7 +462,9 @@ spark_status spark_cross_validate(const spark_cross_params* p);
 spark_status spark_selftest_wait(int64_t limit_ns, cudaStream_t stream);
 
 /* Synchronises the stream, reads and clears the device status word:
- * SPARK_OK, SPARK_ERR_TIMEOUT (a bounded wait expired) or SPARK_ERR_CUDA. */
+ * SPARK_OK, SPARK_ERR_TIMEOUT (a bounded wait expired), SPARK_ERR_CUDA, or
+ * SPARK_ERR_UNSUPPORTED (the data was outside what a call supports, such as a
+ * key_len out of range). */
 spark_status spark_get_status(cudaStream_t stream);
 
 /* Static description of a status code. */
