@@ -26,10 +26,11 @@ constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int ROWS = 16, KEYS = 32, STAGES = 3;
 constexpr int MIN_KEYS = WARPS * KEYS;       // fewest keys worth a block of their own
 constexpr int CLUSTER = 8;                   // most blocks of a tile that join among themselves
-// Weights are 2^(logit - maximum + ABOVE): fp16 ends at 2^16 and loses what is below
-// 2^-25, so that weights down to 2^-40 of the row's largest count in P V as they do
-// in the sum. Statistics hold maximum - ABOVE, what the weights are relative to.
-template <bool H> constexpr float ABOVE = H ? 15.0f : 0.0f;
+// Weights are 2^(logit - reference). fp16 ends at 2^16 and loses what is below 2^-25,
+// so its reference lies 7 below the maximum: weights down to 2^-32 of the largest
+// one a warp has seen count in P V as they do in the sum. However large the maximum,
+// its difference to a 7 is never rounded to more than 8 (15 would become 16).
+template <bool H> constexpr float BELOW = H ? 7.f : 0.f;
 
 struct Args {
   Problem p;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
   for (int n = 0; n < D / 8; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};               // reference, sum
 
   for (int i = 0; i < steps; ++i) {
     const uint32_t kept2 = issue(i + 2);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
       }
     }
     // running softmax; rows lane / 4 and lane / 4 + 8
-    float mx[2] = {m[0], m[1]};
+    float mx[2] = {H ? -INFINITY : m[0], H ? -INFINITY : m[1]};
 #pragma unroll
     for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
     for (int r = 0; r < 2; ++r) {
       mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
       mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      if constexpr (H) mx[r] = fmaxf(m[r], mx[r] - BELOW<H>);
       const float c = mx[r] == -INFINITY ? 1.f : exp2f(m[r] - mx[r]);
       m[r] = mx[r];
       l[r] *= c;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
       }
     }
     // (logits all -inf so far: exp2(-inf - 0) = 0; NaN stays NaN and reaches sum and O)
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - ABOVE<H>, m[1] == -INFINITY ? 0.f : m[1] - ABOVE<H>};
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
     for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
@@ -256,8 +258,8 @@ __global__ void __launch_bounds__(THREADS) kernel(const __grid_constant__ Args a
     if (r0 + 8 < live) *reinterpret_cast<float2*>(so + ((warp * ROWS + r0 + 8) * D + c)) = make_float2(o[n][2], o[n][3]);
   }
   if ((lane & 3) == 0) {
-    ss[warp * ROWS + r0] = make_float2(m[0] - ABOVE<H>, l[0]);
-    ss[warp * ROWS + r0 + 8] = make_float2(m[1] - ABOVE<H>, l[1]);
+    ss[warp * ROWS + r0] = make_float2(m[0], l[0]);
+    ss[warp * ROWS + r0 + 8] = make_float2(m[1], l[1]);
   }
   __syncthreads();
   float* wf = so + WARPS * ROWS * D + 2 * WARPS * ROWS;                 // [WARPS][ROWS] weights of the join

@@ -62,6 +62,10 @@ constexpr int QBUFS = 3;                     // a row tile's Q can load while bo
 // 2^15: those down to 2^-34 of the row's largest count in P V as they do in the sum.
 template <bool H> constexpr float LAZY = H ? 6.0f : 8.0f;
 template <bool H> constexpr float BELOW = H ? 9.0f : 0.0f;
+// (not below it where the logit is so large that the difference would be rounded
+// noticeably, and weights could pass 2^16)
+template <bool H>
+__device__ __forceinline__ float reference(float m) { return H && fabsf(m) < 1048576.f ? m - BELOW<H> : m; }
 constexpr uint32_t O_COL = 256;
 
 struct Args {
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
     for (int it = blockIdx.x; ok && it < a.items; it += gridDim.x) {
       const Item w = item_of(a, it, kept(a, it));
       if (w.tiles == 0 || 2 * w.pair + s >= row_tiles) continue;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, limit = -INFINITY, l = 0.f;      // reference, the logit that moves it, sum
       for (int j = 0; ok && j < w.tiles; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait(s_full(s), ns & 1u, a.status));
         ++ns;
@@ -195,11 +199,14 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ Arg
         auto move = [&](float mt) {
           float corr = 1.f;
           if (m == -INFINITY) {
-            m = mt - BELOW<H>;
-          } else if (mt > m + (BELOW<H> + LAZY<H>)) {
-            corr = ex2(m - (mt - BELOW<H>));
+            m = reference<H>(mt);
+            limit = mt + LAZY<H>;
+          } else if (mt > limit) {
+            limit = mt + LAZY<H>;
+            mt = reference<H>(mt);
+            corr = ex2(m - mt);
             l *= corr;
-            m = mt - BELOW<H>;
+            m = mt;
           }
           if (__any_sync(0xffffffffu, corr != 1.f)) {
             // P_{j-1} V_{j-1} is done (S_j came after it), P_j V_j not issued yet

@@ -426,8 +426,8 @@ typedef struct {
  *   lse          : [B,Hq,Nq] float32 device or NULL
  *   ws           : workspace of spark_cross_workspace_size(p, 0) bytes (scratch;
  *                  calls that may overlap need one each)
- * P is rounded to the tensors' type for P V (fp16: weights below 2^-34 of the
- * row's largest are zero there), sums and statistics are float32 (bf16 values
+ * P is rounded to the tensors' type for P V (fp16: weights below 2^-32 of the
+ * row's largest may be zero there), sums and statistics are float32 (bf16 values
  * past 2^119 / Nk may overflow them).
  * One launch; another before it with a mask and many rows, another behind it
  * where the keys are split over blocks that do not join among themselves. */
